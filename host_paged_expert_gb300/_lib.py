@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, byref, c_double, c_float, c_int32, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, byref, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 import numpy as np
 
@@ -31,6 +31,9 @@ EXPORTS = [
     "pe_load_host_expert", "pe_host_row", "pe_forward", "pe_stats", "pe_read_plan", "pe_read_residency",
     "pe_read_slot", "pe_reset_residency", "pe_probe_host_link", "pe_profile_enable", "pe_profile_read",
     "pe_destroy", "pe_last_error", "pe_expert_mlp_noalloc", "pe_selftest_bounded_waits",
+    "pe_rms_norm", "pe_rms_norm_backward", "pe_rms_norm_backward_workspace", "pe_linear", "pe_linear_backward",
+    "pe_linear_backward_workspace", "pe_gated_ffn", "pe_gated_ffn_workspace", "pe_gated_ffn_backward",
+    "pe_gated_ffn_backward_workspace", "pe_dense_error",
 ]
 
 
@@ -103,6 +106,18 @@ def lib() -> ctypes.CDLL:
     L.pe_destroy.restype = None
     L.pe_expert_mlp_noalloc.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
                                          c_void_p]
+    P, S, N, I = c_void_p, c_int64, c_size_t, c_int32
+    L.pe_rms_norm.argtypes = [P, S, P, S, P, c_float, P, P, P, P, P, I, I, I, P]
+    L.pe_rms_norm_backward.argtypes = [P, S, P, S, P, S, P, P, P, P, P, N, I, I, I, P]
+    L.pe_linear.argtypes = [P, S, P, P, P, P, P, S, P, I, P, I, I, I, I, I, P]
+    L.pe_linear_backward.argtypes = [P, S, P, S, P, P, I, P, P, P, P, N, I, I, I, I, P]
+    L.pe_gated_ffn.argtypes = [P, S, P, P, P, S, P, P, I, P, N, I, I, I, I, P]
+    L.pe_gated_ffn_backward.argtypes = [P, S, P, S, P, P, P, I, P, P, P, P, N, I, I, I, I, P]
+    for name, args in (("pe_rms_norm_backward_workspace", [I, I]), ("pe_linear_backward_workspace", [I, I, I]),
+                       ("pe_gated_ffn_workspace", [I, I]), ("pe_gated_ffn_backward_workspace", [I, I])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = c_size_t
+    L.pe_dense_error.argtypes = [POINTER(c_uint32)]
     L.pe_last_error.argtypes = [c_void_p]
     L.pe_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:

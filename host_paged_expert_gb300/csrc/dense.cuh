@@ -1,0 +1,273 @@
+// Device and host declarations shared by the dense operators (RMS norm,
+// linear, gated feed-forward): element types, activations and the epilogue
+// that every matrix-product kernel applies to eight consecutive columns of a
+// result row.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pe.h"
+
+namespace pe {
+namespace dense {
+
+constexpr int kGroup = 128;  // features sharing one scale of an 8-bit row; rows and columns of a weight block
+
+// What a matrix product does with its accumulators before they are stored.
+enum EpiKind {
+    EPI_LINEAR = 0,     // act(v + bias) + residual; optionally v + bias is kept
+    EPI_GATED = 1,      // act(gate) * up of two accumulators; optionally both are kept
+    EPI_GATED_BWD = 2,  // from dh and the kept gate and up: their gradients and h
+};
+
+struct Epi {
+    int act;             // pe_act
+    int rows, cols;      // valid rows and columns of the result (EPI_GATED*: columns of h)
+    int out_f32;         // EPI_LINEAR: out holds fp32 instead of the element type
+    int vec;             // every row pointer below is 16-byte aligned and cols % 8 = 0
+    void* out;           // EPI_GATED_BWD: [rows, 2 cols], gradients of gate and up
+    int64_t ld_out;
+    const void* bias;    // [cols] or NULL
+    const void* res;     // [rows, cols] or NULL
+    int64_t ld_res;
+    void* keep;          // EPI_LINEAR: [rows, cols] v + bias; EPI_GATED: [rows, 2 cols] gate, up; or NULL
+    int64_t ld_keep;
+    const void* gu;      // EPI_GATED_BWD: [rows, 2 cols] kept gate and up
+    void* h;             // EPI_GATED_BWD: [rows, cols], or NULL
+};
+
+// One matrix product C[m, n] = sum_k A(m, k) B(n, k) with an epilogue.  A
+// and B are row-major matrices in memory: [M, K] (mn = 0) or [K, M] (mn = 1),
+// and likewise for B.  EPI_GATED: B is [2 cols, K], gate rows then up rows.
+struct Product {
+    const void* a;
+    int64_t lda;
+    int a_mn;
+    const void* b;
+    int64_t ldb;
+    int b_mn;
+    int M, N, K;
+    const float* a_scale;  // E4M3 operands: [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]; else NULL
+    const float* b_scale;
+    Epi e;
+};
+
+// elem: pe_elem of the 16-bit operands and of every 16-bit tensor of the epilogue.
+cudaError_t launch_product(const Product& p, EpiKind kind, int elem, uint32_t* err, cudaStream_t st);
+
+struct NormArgs {
+    const void *x, *res, *w;
+    int64_t ld_x, ld_res;
+    float eps;
+    void *y, *sum, *codes;
+    float *scales, *rstd;
+    int rows, hidden;
+};
+cudaError_t launch_rms_norm(const NormArgs& a, int elem, cudaStream_t st);
+
+struct NormBwdArgs {
+    const void *dy, *dsum, *sum, *w;
+    int64_t ld_dy, ld_dsum, ld_sum;
+    const float* rstd;
+    void *dx, *dw;
+    float* partial;  // [norm_bwd_blocks(rows)][hidden]
+    int rows, hidden;
+};
+int norm_bwd_blocks(int rows);
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int elem, cudaStream_t st);
+
+// dz = dy * act'(z) (written with row pitch ld_dz when dz is not NULL) and
+// its column sums (db, when not NULL).
+struct ActBwdArgs {
+    const void *dy, *z;
+    int64_t ld_dy, ld_z;
+    void* dz;
+    int64_t ld_dz;
+    void* db;
+    float* partial;  // [act_bwd_chunks(rows)][cols], when db is not NULL
+    int act, rows, cols;
+};
+int act_bwd_chunks(int rows);
+cudaError_t launch_act_bwd(const ActBwdArgs& a, int elem, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+template <typename E>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+    static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<__half> {
+    static __device__ __forceinline__ float2 unpack(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 p = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+    static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+
+// Eight consecutive elements at p[0..7].  vec: p is 16-byte aligned and all
+// eight exist; else the first n of them are touched one by one.
+template <typename E>
+__device__ __forceinline__ void load8(const E* p, bool vec, int n, float (&v)[8]) {
+    if (vec) {
+        const int4 r = *reinterpret_cast<const int4*>(p);
+        const uint32_t w[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Elem<E>::unpack(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<E>::get(p[i]) : 0.f;
+    }
+}
+template <typename E>
+__device__ __forceinline__ void store8(E* p, bool vec, int n, const float (&v)[8]) {
+    if (vec) {
+        int4 r;
+        r.x = (int)Elem<E>::pack(v[0], v[1]);
+        r.y = (int)Elem<E>::pack(v[2], v[3]);
+        r.z = (int)Elem<E>::pack(v[4], v[5]);
+        r.w = (int)Elem<E>::pack(v[6], v[7]);
+        *reinterpret_cast<int4*>(p) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = Elem<E>::put(v[i]);
+    }
+}
+__device__ __forceinline__ void store8_f32(float* p, bool vec, int n, const float (&v)[8]) {
+    if (vec) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+
+// tanh(x) = 1 - 2 / (1 + e^2x): about 1e-7 absolute, enough for results that
+// are rounded to 16 bits; saturates to +-1.
+__device__ __forceinline__ float tanh_f(float x) { return 1.f - __fdividef(2.f, 1.f + __expf(2.f * x)); }
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+constexpr float kSqrt2OverPi = 0.7978845608028654f;
+constexpr float kGeluCubic = 0.044715f;
+
+// act(z)
+__device__ __forceinline__ float act_fwd(int act, float z) {
+    switch (act) {
+        case PE_ACT_SILU: return z * sigmoid_f(z);
+        case PE_ACT_GELU: return z * (0.5f + 0.5f * erff(z * 0.70710678118654752f));
+        case PE_ACT_GELU_TANH: return z * (0.5f + 0.5f * tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+        case PE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
+        default: return z;
+    }
+}
+// act(z) and its slope d at z
+__device__ __forceinline__ float act_both(int act, float z, float& d) {
+    switch (act) {
+        case PE_ACT_SILU: {
+            const float s = sigmoid_f(z);
+            d = s * (1.f + z * (1.f - s));
+            return z * s;
+        }
+        case PE_ACT_GELU: {
+            const float c = 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+            d = c + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
+            return z * c;
+        }
+        case PE_ACT_GELU_TANH: {
+            const float t = tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+            d = 0.5f + 0.5f * t + 0.5f * z * (1.f - t * t) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+            return z * (0.5f + 0.5f * t);
+        }
+        case PE_ACT_RELU: d = z > 0.f ? 1.f : 0.f; return z > 0.f ? z : (z != z ? z : 0.f);
+        default: d = 1.f; return z;
+    }
+}
+
+// The epilogue of columns col..col+7 of row `row`: v the accumulators (of
+// gate for EPI_GATED, where u holds up's; of dh for EPI_GATED_BWD).  The one
+// rounding to 16 bits is at each store.
+template <typename E, int KIND>
+__device__ __forceinline__ void epilogue8(const Epi& e, int row, int col, float (&v)[8], const float (&u)[8]) {
+    const int n = e.cols - col;
+    if (row >= e.rows || n <= 0) return;
+    const bool vec = e.vec != 0;  // cols % 8 = 0: all eight exist
+    if (KIND == EPI_LINEAR) {
+        if (e.bias) {
+            float b[8];
+            load8(static_cast<const E*>(e.bias) + col, vec, n, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += b[i];
+        }
+        if (e.keep) store8(static_cast<E*>(e.keep) + row * e.ld_keep + col, vec, n, v);
+        if (e.act != PE_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_fwd(e.act, v[i]);
+        }
+        if (e.res) {
+            float r[8];
+            load8(static_cast<const E*>(e.res) + row * e.ld_res + col, vec, n, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        if (e.out_f32) store8_f32(static_cast<float*>(e.out) + row * e.ld_out + col, vec, n, v);
+        else store8(static_cast<E*>(e.out) + row * e.ld_out + col, vec, n, v);
+    } else if (KIND == EPI_GATED) {
+        if (e.keep) {
+            E* k = static_cast<E*>(e.keep) + row * e.ld_keep + col;
+            store8(k, vec, n, v);
+            store8(k + e.cols, vec, n, u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_fwd(e.act, v[i]) * u[i];
+        store8(static_cast<E*>(e.out) + row * e.ld_out + col, vec, n, v);
+    } else {
+        const E* p = static_cast<const E*>(e.gu) + row * e.ld_keep + col;
+        float g[8], w[8];
+        load8(p, vec, n, g);
+        load8(p + e.cols, vec, n, w);
+        float dg[8], du[8], h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float d;
+            const float a = act_both(e.act, g[i], d);
+            dg[i] = v[i] * w[i] * d;
+            du[i] = v[i] * a;
+            h[i] = a * w[i];
+        }
+        E* o = static_cast<E*>(e.out) + row * e.ld_out + col;
+        store8(o, vec, n, dg);
+        store8(o + e.cols, vec, n, du);
+        if (e.h) store8(static_cast<E*>(e.h) + row * (int64_t)e.cols + col, vec, n, h);
+    }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace dense
+}  // namespace pe

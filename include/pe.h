@@ -332,6 +332,133 @@ pe_status pe_profile_read(pe_handle* h, pe_profile_t* out);
 pe_status pe_expert_mlp_noalloc(const void* w13, const void* w2, const void* x, void* out,
                                 int32_t num_tokens, int32_t hidden, int32_t intermediate, void* stream);
 
+/* ---- Dense operators around a paged layer --------------------------------
+ *
+ * What a decoder layer runs next to its routed experts: the RMS norm in front
+ * of them, the products that have no routing (the attention's output
+ * projection, the router's logits that pe_forward takes) and the gated
+ * feed-forward block of a shared expert or a dense layer.  The pages leave all
+ * of these to the model; the weight layouts are those of the expert rows
+ * (w13 = gate rows then up rows; block-FP8 scales per 128 x 128 block).
+ *
+ * Conventions:
+ *   - No handle, no host synchronisation, no allocation: asynchronous on
+ *     `stream`, capturable in a CUDA graph.  Workspaces are the caller's,
+ *     256-byte aligned, and may be reused once the call's kernels are done.
+ *   - Matrices are row-major.  Activations that a call reads have a row
+ *     pitch in elements (`*_stride`, at least the row's length); what it
+ *     writes, weights and scales are contiguous.  Pointers are 16-byte
+ *     aligned, pitches multiples of 16 bytes (a row length that is no
+ *     multiple of 8, allowed for a product's outputs alone, needs a contiguous
+ *     residual instead).  Outputs may not overlap inputs or each other.
+ *   - Sums, norms and accumulators are fp32; a result is rounded to its type
+ *     once, when it is stored.
+ *   - rows = 0 is a no-op, except that weight gradients are then set to zero.
+ *   - Results do not depend on timing: the same call gives the same bits.
+ *   - Errors: PE_ERR_INVALID (NULL, misaligned, bad sizes or types),
+ *     PE_ERR_RANGE (above a stated limit), PE_ERR_CUDA; the message is in
+ *     pe_last_error(NULL). */
+typedef enum pe_elem {
+    PE_ELEM_BF16 = 0,
+    PE_ELEM_F16 = 1,
+    PE_ELEM_F32 = 2   /* pe_linear's out only */
+} pe_elem;
+
+typedef enum pe_act {
+    PE_ACT_NONE = 0,
+    PE_ACT_SILU = 1,      /* z / (1 + e^-z)                                  */
+    PE_ACT_GELU = 2,      /* z Phi(z)                                        */
+    PE_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))    */
+    PE_ACT_RELU = 4
+} pe_act;
+
+/* Features that share one scale of an 8-bit row. */
+#define PE_SCALE_GROUP 128
+
+/* RMS norm of x + residual:
+ *   s = x + residual (x alone if residual is NULL),
+ *   r = 1 / sqrt(mean(s^2) + eps) of each row,   y = s * r * weight.
+ *   sum:    [rows, hidden] s rounded to elem (the new residual stream), or NULL
+ *   y:      [rows, hidden], or NULL
+ *   codes, scales: y in 8 bits, or both NULL: E4M3 codes [rows, hidden] and
+ *           fp32 scales [rows, ceil(hidden/128)]; y = code * scale, scale =
+ *           max|y| / 448 over the 128 features (1 where all are zero)
+ *   rstd:   [rows] r, for the backward pass, or NULL
+ * y is computed from the unrounded s.  hidden: a multiple of 8, at most 32768. */
+pe_status pe_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                      const void* weight, float eps, void* y, void* sum, void* codes, float* scales, float* rstd,
+                      int32_t rows, int32_t hidden, int32_t elem, void* stream);
+
+/* Its gradients.  sum and rstd are the forward call's (sum = x where it had
+ * no residual); dy the gradient of y, dsum that of sum (NULL: zero).
+ *   dx: [rows, hidden], the gradient of x and of the residual alike;
+ *   dweight: [hidden].
+ * workspace: pe_rms_norm_backward_workspace(rows, hidden) bytes. */
+size_t pe_rms_norm_backward_workspace(int32_t rows, int32_t hidden);
+pe_status pe_rms_norm_backward(const void* dy, int64_t dy_stride, const void* dsum, int64_t dsum_stride,
+                               const void* sum, int64_t sum_stride, const void* weight, const float* rstd, void* dx,
+                               void* dweight, void* workspace, size_t workspace_bytes, int32_t rows, int32_t hidden,
+                               int32_t elem, void* stream);
+
+/* out = act(x weight^T + bias) + residual.
+ *   x: [rows, in], weight: [out, in]; bias: [out] or NULL; residual, out: [rows, out].
+ *   x_scale, w_scale: NULL (x and weight of type elem), or both the scales of
+ *     E4M3 x and weight: x_scale [rows, ceil(in/128)] as pe_rms_norm writes
+ *     them, w_scale [ceil(out/128), ceil(in/128)].
+ *   keep: [rows, out] x weight^T + bias rounded to elem, for the backward
+ *     pass, or NULL.
+ *   elem: type of bias, residual and keep (and of x and weight without
+ *     scales); out_elem: elem or PE_ELEM_F32.
+ * in: a multiple of 8 (of 16 for E4M3). */
+pe_status pe_linear(const void* x, int64_t x_stride, const float* x_scale, const void* weight, const float* w_scale,
+                    const void* bias, const void* residual, int64_t residual_stride, void* out, int32_t out_elem,
+                    void* keep, int32_t act, int32_t rows, int32_t in_features, int32_t out_features, int32_t elem,
+                    void* stream);
+
+/* Gradients of pe_linear (without scales): with dz = dy * act'(keep),
+ *   dx = dz weight [rows, in], dweight = dz^T x [out, in], dbias = column
+ *   sums of dz [out]; each may be NULL.  The residual's gradient is dy.
+ * keep may be NULL for PE_ACT_NONE.
+ * workspace: pe_linear_backward_workspace(rows, out, act) bytes. */
+size_t pe_linear_backward_workspace(int32_t rows, int32_t out_features, int32_t act);
+pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
+                             const void* keep, int32_t act, void* dx, void* dweight, void* dbias, void* workspace,
+                             size_t workspace_bytes, int32_t rows, int32_t in_features, int32_t out_features,
+                             int32_t elem, void* stream);
+
+/* Gated feed-forward block: h = act(x gate^T) * (x up^T) in one kernel,
+ * out = h w2^T + residual in a second.
+ *   x, residual, out: [rows, hidden]; w13: [2 intermediate, hidden] (gate rows,
+ *   then up rows); w2: [hidden, intermediate].
+ *   keep: [rows, 2 intermediate] x gate^T and x up^T rounded to elem, for the
+ *     backward pass, or NULL.
+ * h is rounded to elem between the two products.
+ * workspace: pe_gated_ffn_workspace(rows, intermediate) bytes.
+ * hidden, intermediate: multiples of 8. */
+size_t pe_gated_ffn_workspace(int32_t rows, int32_t intermediate);
+pe_status pe_gated_ffn(const void* x, int64_t x_stride, const void* w13, const void* w2, const void* residual,
+                       int64_t residual_stride, void* out, void* keep, int32_t act, void* workspace,
+                       size_t workspace_bytes, int32_t rows, int32_t hidden, int32_t intermediate, int32_t elem,
+                       void* stream);
+
+/* Gradients of pe_gated_ffn.  With dh = dy w2 and the kept g = gate, u = up:
+ *   dg = dh u act'(g), du = dh act(g),  dx = dg gate + du up,
+ *   dw13 = [dg du]^T x,  dw2 = dy^T h (h recomputed from g and u);
+ * each of dx, dw13 and dw2 may be NULL.  The residual's gradient is dy.
+ * dg, du and h are rounded to elem in between.
+ * workspace: pe_gated_ffn_backward_workspace(rows, intermediate) bytes. */
+size_t pe_gated_ffn_backward_workspace(int32_t rows, int32_t intermediate);
+pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* w13,
+                                const void* w2, const void* keep, int32_t act, void* dx, void* dw13, void* dw2,
+                                void* workspace, size_t workspace_bytes, int32_t rows, int32_t hidden,
+                                int32_t intermediate, int32_t elem, void* stream);
+
+/* Error word of the dense operators on the current device: 0, or
+ * PE_DEVERR_TIMEOUT once a bounded wait inside one of their kernels gave up
+ * (that call's results are then incomplete).  Sticky.  Synchronises the
+ * device. */
+pe_status pe_dense_error(uint32_t* word);
+
 /* Frees the host store (if owned) and the handle; never the arena. */
 void pe_destroy(pe_handle* h);
 
