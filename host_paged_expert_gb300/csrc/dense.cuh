@@ -9,7 +9,12 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <limits.h>
 #include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "pe.h"
 
@@ -59,6 +64,8 @@ struct Product {
 
 // elem: pe_elem of the 16-bit operands and of every 16-bit tensor of the epilogue.
 cudaError_t launch_product(const Product& p, EpiKind kind, int elem, uint32_t* err, cudaStream_t st);
+
+using PFN_encode = PFN_cuTensorMapEncodeTiled_v12000;
 
 struct NormArgs {
     const void *x, *res, *w;

@@ -1,0 +1,120 @@
+// PTX wrappers for the dense operators' tensor-core kernels, beyond those of
+// tc_sm100.cuh: CTA pairs (cta_group::2), operands whose rows are contiguous
+// along M or N, 8-bit operands, clusters.
+#pragma once
+
+#include "tc_sm100.cuh"
+
+namespace pe {
+namespace tc {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Waits for a barrier phase without sleeping in between; bounded (a poll
+// suspends the thread for up to a microsecond or so by itself).
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, uint32_t* err) {
+    for (uint32_t i = 0; i < (1u << 22); ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    atomicOr(err, (uint32_t)PE_DEVERR_TIMEOUT);
+    return false;
+}
+
+// Loads a box into this CTA's shared memory; the bytes count on `bar`, a
+// shared::cluster address (of either CTA of the pair).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// One MMA over a CTA pair (PAIR) or one CTA; FP8: E4M3 operands, 32 deep,
+// else 16-bit operands, 16 deep.
+template <bool PAIR, bool FP8>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+#define PE_MMA(G, KIND)                                                                                     \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                           \
+                 "tcgen05.mma.cta_group::" G ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),      \
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                                      \
+                 : "memory")
+    if (PAIR && FP8) PE_MMA("2", "f8f6f4");
+    else if (PAIR) PE_MMA("2", "f16");
+    else if (FP8) PE_MMA("1", "f8f6f4");
+    else PE_MMA("1", "f16");
+#undef PE_MMA
+}
+
+// Arrive on `bar` of both CTAs of the pair once the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Shared-memory descriptor of an operand tile written by TMA with 128-byte
+// swizzling.
+//   K-major: rows of 128 bytes along K, 1024-byte groups of 8 rows.  A step
+//   along K inside the row adds its bytes to the address.
+//   MN-major: boxes of 64 elements along M or N by 64 along K (8192 bytes,
+//   one 128-byte row per k); the leading offset steps to the next box of 64,
+//   the stride offset to the next 8 k.  A step of 16 k adds 2048 bytes.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn) {
+    uint64_t d = smem_desc_sw128(saddr);
+    if (mn) d = (d & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(8192 >> 4) << 16);
+    return d;
+}
+
+// Instruction descriptor: fp32 accumulators, A and B of one type.
+//   fmt: kind::f16: 0 fp16, 1 bf16; kind::f8f6f4: 0 E4M3.
+__host__ __device__ constexpr uint32_t idesc(int fmt, int a_mn, int b_mn, int M, int N) {
+    return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <int R>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+}  // namespace tc
+}  // namespace pe

@@ -1,90 +1,363 @@
 // Matrix products of the dense operators: C[m, n] = sum_k A(m, k) B(n, k),
-// then the epilogue.  A first, plain form: 64 x 64 tiles of C per block,
-// 16-deep slices of both operands widened to fp32 in shared memory, 4 x 4
-// accumulators per thread.
+// then the epilogue.
+//
+// pair_kernel: persistent CTA pairs (two SMs), 256 x 256 tiles of C.  Each
+// CTA's TMA producer streams its half of A and of B (128 rows x 128 bytes
+// each, 128-byte swizzle) into a ring of stages; one thread of the pair's
+// leader issues the 256 x 256 tcgen05.mma, which reads both CTAs' shared
+// memory, so a byte of B feeds 256 rows instead of 128.  Accumulators live in
+// TMEM, two buffers of 256 columns, so that eight epilogue warps drain one
+// tile while the next is multiplied.  Each epilogue warp turns its 32 x 32
+// blocks through a swizzled shared-memory patch, after which eight lanes hold
+// eight rows' 64 contiguous bytes and every load and store of the epilogue is
+// coalesced.
+//
+// Operands may be row-major along K or along M / N (the backward products
+// read the same tensors transposed): both have a swizzled layout that the
+// MMA's descriptors name, so nothing is transposed in memory.
+//
+// E4M3 operands: a stage is 128 deep, one scale group.  Each stage's product
+// goes to its own TMEM buffer and the epilogue warps add it, times the row's
+// and the block's scale, to fp32 accumulators in registers, while the next
+// stage is multiplied.
 #include "dense.cuh"
+#include "dense_tc.cuh"
+#include "pe_device.cuh"
 
 namespace pe {
 namespace dense {
+
+PFN_encode encode_fn();
+
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16;
+constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 2 TMEM, 4..11 epilogue
+constexpr int kTile = 256;             // rows and columns of C per CTA pair
+constexpr int kHalf = 128;             // operand rows per CTA
+constexpr int kOperand = kHalf * 128;  // bytes of one operand's stage
+constexpr int kStage = 2 * kOperand;
+constexpr int kRaster = 8;             // tile rows walked together, so that their B tiles are shared in L2
 
-template <typename E>
-__device__ __forceinline__ float fetch(const void* p, int64_t ld, int mn, int r, int k, const float* scale, int rows_per,
-                                       int groups) {
-    const size_t at = mn ? (size_t)k * ld + r : (size_t)r * ld + k;
-    if (scale) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const __nv_fp8_storage_t*>(p)[at], __NV_E4M3);
-        return __half2float(__half(h)) * scale[(size_t)(r / rows_per) * groups + k / kGroup];
-    }
-    return Elem<E>::get(static_cast<const E*>(p)[at]);
+constexpr int patch_bytes(int kind) { return kind == EPI_GATED ? 8192 : 4096; }
+constexpr int stages(int kind) { return kind == EPI_GATED ? 5 : 6; }
+constexpr int smem_bytes(int kind) { return 1024 + stages(kind) * kStage + 8 * patch_bytes(kind); }
+
+// Registers: 128 x (72 + 2 x 216) = 384 x 168, what the block is launched with.
+constexpr int kRegsFew = 72, kRegsMany = 216;
+
+struct Shared {
+    uint64_t full[6], empty[6], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+};
+
+// One warp's 32 x 32 fp32 block, lane = row: to the patch, rows of 128 bytes
+// whose 16-byte chunks are XOR-swizzled by the row.
+__device__ __forceinline__ void patch_put(uint8_t* patch, int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(patch + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+}
+// Eight columns 8 c8 .. of row r.
+__device__ __forceinline__ void patch_get(const uint8_t* patch, int r, int c8, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(patch + r * 128 + (((2 * c8) ^ (r & 7)) << 4));
+    const float4 b = *reinterpret_cast<const float4*>(patch + r * 128 + (((2 * c8 + 1) ^ (r & 7)) << 4));
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
 template <typename E, int KIND>
-__global__ void __launch_bounds__(256) product_kernel(const Product p) {
-    __shared__ float sa[TK][TM + 1], sb[TK][TN + 1], su[TK][TN + 1];
-    __shared__ float c[2][TM][TN + 4];
-    const int m0 = blockIdx.x * TM, n0 = blockIdx.y * TN;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int groups = (p.K + kGroup - 1) / kGroup;
-    const int N = KIND == EPI_GATED ? p.e.cols : p.N;
-    float acc[4][4] = {}, acu[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += TK) {
-        for (int i = threadIdx.x; i < TM * TK; i += 256) {
-            const int r = p.a_mn ? i % TM : i / TK, k = p.a_mn ? i / TM : i % TK;
-            sa[k][r] = m0 + r < p.M && k0 + k < p.K ? fetch<E>(p.a, p.lda, p.a_mn, m0 + r, k0 + k, p.a_scale, 1, groups) : 0.f;
-        }
-        for (int i = threadIdx.x; i < TN * TK; i += 256) {
-            const int r = p.b_mn ? i % TN : i / TK, k = p.b_mn ? i / TN : i % TK;
-            const bool in = n0 + r < N && k0 + k < p.K;
-            sb[k][r] = in ? fetch<E>(p.b, p.ldb, p.b_mn, n0 + r, k0 + k, p.b_scale, kGroup, groups) : 0.f;
-            if (KIND == EPI_GATED) su[k][r] = in ? fetch<E>(p.b, p.ldb, 0, N + n0 + r, k0 + k, nullptr, 1, 1) : 0.f;
-        }
-        __syncthreads();
+__device__ __forceinline__ void patch_out(const Epi& e, uint8_t* patch, int lane, int row0, int col0) {
 #pragma unroll
-        for (int k = 0; k < TK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-                    if (KIND == EPI_GATED) acu[i][j] = fmaf(sa[k][ty * 4 + i], su[k][tx * 4 + j], acu[i][j]);
-                }
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            c[0][ty * 4 + i][tx * 4 + j] = acc[i][j];
-            c[1][ty * 4 + i][tx * 4 + j] = acu[i][j];
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < TM * TN / 8; i += 256) {
-        const int r = i / (TN / 8), q = (i % (TN / 8)) * 8;
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 8 + (lane >> 2), c8 = lane & 3;
         float v[8], u[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = c[0][r][q + j];
-            u[j] = c[1][r][q + j];
-        }
-        epilogue8<E, KIND>(p.e, m0 + r, n0 + q, v, u);
+        patch_get(patch, r, c8, v);
+        if (KIND == EPI_GATED) patch_get(patch + 4096, r, c8, u);
+        epilogue8<E, KIND>(e, row0 + r, col0 + 8 * c8, v, u);
     }
 }
 
+struct Tiles {
+    int tm, tn, total;
+    __device__ __forceinline__ void at(int t, int& m, int& n) const {
+        const int per = kRaster * tn, first = t / per * kRaster, rows = min(kRaster, tm - first), r = t % per;
+        m = first + r % rows;
+        n = r / rows;
+    }
+};
+
+template <typename E, int KIND, bool FP8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const __grid_constant__ Product p, uint32_t* err) {
+    constexpr int STAGES = stages(KIND);
+    constexpr int BK = FP8 ? 128 : 64;                      // elements of a 128-byte row
+    constexpr int NT = KIND == EPI_GATED ? kTile / 2 : kTile;  // result columns of a tile
+    extern __shared__ uint8_t dyn[];
+    __shared__ Shared S;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    Tiles tiles;
+    tiles.tm = (p.M + kTile - 1) / kTile;
+    tiles.tn = (p.e.cols + NT - 1) / NT;
+    tiles.total = tiles.tm * tiles.tn;
+    const int kblocks = (p.K + BK - 1) / BK;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            tc::mbar_init(&S.full[i], 1);
+            tc::mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&S.acc_full[i], 1);
+            tc::mbar_init(&S.acc_empty[i], 16);  // eight epilogue warps of each CTA
+        }
+        tc::mbar_init(&S.drain, 1);
+        tc::fence_barrier_init();
+        tc::tma_prefetch(&ta);
+        tc::tma_prefetch(&tb);
+    }
+    if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_arrive();
+    tc::cluster_wait();
+    tc::fence_after_sync();
+    const uint32_t tmem = S.tmem;
+    pdl_wait();
+
+    if (warp < 4) {
+        if (FP8) tc::reg_dec<kRegsFew>();
+    if (warp == 0 && lane == 0) {
+        // ---- producer
+        uint32_t pos = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles.total && ok; t += pairs) {
+            int mt, nt;
+            tiles.at(t, mt, nt);
+            const int m0 = mt * kTile + (int)rank * kHalf;
+            const int n0 = KIND == EPI_GATED ? (int)rank * p.e.cols + nt * NT : nt * NT + (int)rank * kHalf;
+            for (int kb = 0; kb < kblocks; ++kb, ++pos) {
+                const uint32_t s = pos % STAGES, use = pos / STAGES;
+                if (!(ok = tc::mbar_spin(&S.empty[s], (use & 1) ^ 1, err))) break;
+                if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * kStage);
+                const uint32_t bar = tc::map_rank(tc::smem_u32(&S.full[s]), 0);
+                uint8_t* a = ring + s * kStage;
+                uint8_t* b = a + kOperand;
+                if (p.a_mn) {
+                    tc::tma_load_2d_pair(a, &ta, bar, m0, kb * BK);
+                    tc::tma_load_2d_pair(a + 8192, &ta, bar, m0 + 64, kb * BK);
+                } else {
+                    tc::tma_load_2d_pair(a, &ta, bar, kb * BK, m0);
+                }
+                if (p.b_mn) {
+                    tc::tma_load_2d_pair(b, &tb, bar, n0, kb * BK);
+                    tc::tma_load_2d_pair(b + 8192, &tb, bar, n0 + 64, kb * BK);
+                } else {
+                    tc::tma_load_2d_pair(b, &tb, bar, kb * BK, n0);
+                }
+            }
+        }
+        // after a wait gave up: let this pair's copies land before the block ends
+        if (!ok && rank == 0)
+            for (uint32_t i = pos > STAGES ? pos - STAGES : 0; i < pos; ++i)
+                tc::mbar_wait(&S.full[i % STAGES], (i / STAGES) & 1, err, PE_DEVERR_TIMEOUT, 1u << 16);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- MMA issuer
+        constexpr int FMT = FP8 ? 0 : std::is_same<E, __nv_bfloat16>::value ? 1 : 0;
+        const uint32_t id = tc::idesc(FMT, p.a_mn, p.b_mn, kTile, kTile);
+        const uint32_t astep = p.a_mn ? 2048 : 32, bstep = p.b_mn ? 2048 : 32;
+        uint32_t pos = 0, use_acc = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles.total && ok; t += pairs) {
+            for (int kb = 0; kb < kblocks; ++kb, ++pos) {
+                const uint32_t buf = use_acc & 1;
+                if (FP8 || kb == 0) {
+                    if (!(ok = tc::mbar_spin(&S.acc_empty[buf], ((use_acc >> 1) & 1) ^ 1, err))) break;
+                }
+                const uint32_t s = pos % STAGES;
+                if (!(ok = tc::mbar_spin(&S.full[s], (pos / STAGES) & 1, err))) break;
+                tc::fence_after_sync();
+                const uint32_t a = tc::smem_u32(ring + s * kStage), b = a + kOperand;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma<true, FP8>(tmem + buf * kTile, tc::operand_desc(a + k * astep, p.a_mn),
+                                       tc::operand_desc(b + k * bstep, p.b_mn), id, (!FP8 && kb) || k);
+                tc::mma_commit_pair(&S.empty[s]);
+                if (FP8 || kb == kblocks - 1) {
+                    tc::mma_commit_pair(&S.acc_full[buf]);
+                    ++use_acc;
+                }
+            }
+        }
+        if (!ok) {  // the MMAs already issued read shared memory and write TMEM
+            tc::mma_commit_pair(&S.drain);
+            tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, 1u << 16);
+        }
+    }
+    } else {
+        // ---- epilogue
+        if (FP8) tc::reg_inc<kRegsMany>();
+        const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
+        uint8_t* patch = ring + STAGES * kStage + ew * patch_bytes(KIND);
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t release = tc::map_rank(tc::smem_u32(&S.acc_empty[0]), 0);  // of the pair's leader
+        uint32_t use_acc = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles.total && ok; t += pairs) {
+            int mt, nt;
+            tiles.at(t, mt, nt);
+            const int row0 = mt * kTile + (int)rank * kHalf + quarter * 32;
+            if (FP8) {
+                float acc[128];
+#pragma unroll
+                for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+                const int row = row0 + lane, nb = (nt * NT + half * 128) / kGroup;
+                const bool live = row < p.M && nt * NT + half * 128 < p.N;
+                const float* as = p.a_scale + (size_t)(live ? row : 0) * kblocks;
+                const float* bs = p.b_scale + (size_t)(live ? nb : 0) * kblocks;
+                for (int kb = 0; kb < kblocks; ++kb, ++use_acc) {
+                    const float sc = live ? __ldg(as + kb) * __ldg(bs + kb) : 0.f;
+                    const uint32_t buf = use_acc & 1;
+                    if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(lanes + buf * kTile + half * 128 + c * 32, r);
+                        tc::tmem_ld_wait();
+                        if (c == 3) {
+                            tc::fence_before_sync();
+                            if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sc, acc[c * 32 + i]);
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c * 32 + i]);
+                    __syncwarp();
+                    patch_put(patch, lane, r);
+                    __syncwarp();
+                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + half * 128 + c * 32);
+                }
+            } else {
+                const uint32_t buf = use_acc & 1;
+                if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
+                ++use_acc;
+                tc::fence_after_sync();
+                constexpr int CH = NT / 64;  // 32-column chunks of this warp's half
+#pragma unroll 1
+                for (int c = 0; c < CH; ++c) {
+                    const int col = half * (NT / 2) + c * 32;
+                    uint32_t r[32];
+                    tc::tmem_ld32(lanes + buf * kTile + col, r);
+                    tc::tmem_ld_wait();
+                    __syncwarp();  // the patch's last readers are done
+                    patch_put(patch, lane, r);
+                    if (KIND == EPI_GATED) {
+                        tc::tmem_ld32(lanes + buf * kTile + kTile / 2 + col, r);
+                        tc::tmem_ld_wait();
+                        patch_put(patch + 4096, lane, r);
+                    }
+                    if (c == CH - 1) {
+                        tc::fence_before_sync();
+                        if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
+                    }
+                    __syncwarp();
+                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + col);
+                }
+            }
+        }
+    }
+    // neither CTA leaves, and no TMEM is freed, while the other may still use it
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_arrive();
+    tc::cluster_wait();
+    tc::fence_after_sync();
+    if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+bool encode(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t es = fp8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)(mn ? rows : k), (cuuint64_t)(mn ? k : rows)};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {fp8 ? 128u : 64u, mn ? 64u : (cuuint32_t)kHalf};
+    const cuuint32_t step[2] = {1, 1};
+    // the type only sizes the elements: nothing is converted on the way
+    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
+              strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs that the device holds at once, looked up once per kernel.
+template <typename E, int KIND, bool FP8>
+cudaError_t resident_pairs(int* out) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    int n = dev < 64 ? known[dev].load() : 0;
+    if (!n) {
+        auto k = pair_kernel<E, KIND, FP8>;
+        if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND))) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem_bytes(KIND);
+        if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        if (dev < 64) known[dev].store(n);
+    }
+    *out = n;
+    return cudaSuccess;
+}
+
+template <typename E, int KIND, bool FP8>
+cudaError_t launch(const Product& p, uint32_t* err, cudaStream_t st) {
+    CUtensorMap ta, tb;
+    if (!encode(&ta, p.a, p.lda, p.M, p.K, p.a_mn, FP8) || !encode(&tb, p.b, p.ldb, p.N, p.K, p.b_mn, FP8))
+        return cudaErrorInvalidValue;
+    int pairs = 0;
+    if (cudaError_t e = resident_pairs<E, KIND, FP8>(&pairs)) return e;
+    const long long nt = KIND == EPI_GATED ? kTile / 2 : kTile;
+    const long long tiles = (long long)((p.M + kTile - 1) / kTile) * ((p.e.cols + nt - 1) / nt);
+    if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
+    if (tiles < pairs) pairs = (int)tiles;
+    return launch_pdl(pair_kernel<E, KIND, FP8>, dim3(2 * pairs), dim3(kThreads), smem_bytes(KIND), st, ta, tb, p, err);
+}
+
 template <typename E>
-cudaError_t launch(const Product& p, EpiKind kind, cudaStream_t st) {
-    const int N = kind == EPI_GATED ? p.e.cols : p.N;
-    const dim3 grid((p.M + TM - 1) / TM, (N + TN - 1) / TN);
-    if (kind == EPI_LINEAR) product_kernel<E, EPI_LINEAR><<<grid, 256, 0, st>>>(p);
-    else if (kind == EPI_GATED) product_kernel<E, EPI_GATED><<<grid, 256, 0, st>>>(p);
-    else product_kernel<E, EPI_GATED_BWD><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_kind(const Product& p, EpiKind kind, uint32_t* err, cudaStream_t st) {
+    if (p.a_scale) return launch<E, EPI_LINEAR, true>(p, err, st);
+    if (kind == EPI_LINEAR) return launch<E, EPI_LINEAR, false>(p, err, st);
+    if (kind == EPI_GATED) return launch<E, EPI_GATED, false>(p, err, st);
+    return launch<E, EPI_GATED_BWD, false>(p, err, st);
 }
 
 }  // namespace
 
-cudaError_t launch_product(const Product& p, EpiKind kind, int elem, uint32_t*, cudaStream_t st) {
-    return elem == PE_ELEM_BF16 ? launch<__nv_bfloat16>(p, kind, st) : launch<__half>(p, kind, st);
+PFN_encode encode_fn() {
+    static PFN_encode fn = [] {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r);
+        return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_encode>(q) : nullptr;
+    }();
+    return fn;
+}
+
+cudaError_t launch_product(const Product& p, EpiKind kind, int elem, uint32_t* err, cudaStream_t st) {
+    return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, err, st) : launch_kind<__half>(p, kind, err, st);
 }
 
 }  // namespace dense
