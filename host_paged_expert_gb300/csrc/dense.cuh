@@ -62,8 +62,26 @@ struct Product {
     Epi e;
 };
 
+// Place of a product in a chain of launches of one call: CHAIN_BEFORE: the
+// next launch is a product whose B does not depend on this one; CHAIN_AFTER:
+// this product's B does not depend on the launch before it, whose own
+// predecessors are done by the time it lets this one start.
+enum { CHAIN_NONE = 0, CHAIN_BEFORE = 1, CHAIN_AFTER = 2 };
+
 // elem: pe_elem of the 16-bit operands and of every 16-bit tensor of the epilogue.
-cudaError_t launch_product(const Product& p, EpiKind kind, int elem, uint32_t* err, cudaStream_t st);
+cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, uint32_t* err, cudaStream_t st);
+
+// The two kernels behind launch_product: tiles of 256 rows x tn (256 or 128)
+// columns on CTA pairs, and tiles of 128 columns x nt rows whose K axis a
+// cluster of `split` CTAs shares.
+struct SplitShape {
+    int nt, split;
+};
+cudaError_t launch_pairs(const Product& p, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st);
+cudaError_t launch_split(const Product& p, EpiKind kind, int elem, const SplitShape& s, int chain, uint32_t* err,
+                         cudaStream_t st);
+// K blocks of 64 that one accumulator takes where the result is fp32, of kb in all.
+int split_blocks(const SplitShape& s, int kb);
 
 using PFN_encode = PFN_cuTensorMapEncodeTiled_v12000;
 
@@ -216,61 +234,125 @@ __device__ __forceinline__ float act_both(int act, float z, float& d) {
     }
 }
 
-// The epilogue of columns col..col+7 of row `row`: v the accumulators (of
-// gate for EPI_GATED, where u holds up's; of dh for EPI_GATED_BWD).  The one
-// rounding to 16 bits is at each store.
+// act of eight values (one branch for all of them)
+__device__ __forceinline__ void act_fwd8(int act, float (&v)[8]) {
+#define PE_ACT8(A)                                              \
+    case A:                                                     \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = act_fwd(A, v[i]); \
+        break
+    switch (act) {
+        PE_ACT8(PE_ACT_SILU);
+        PE_ACT8(PE_ACT_GELU);
+        PE_ACT8(PE_ACT_GELU_TANH);
+        PE_ACT8(PE_ACT_RELU);
+        default: break;
+    }
+#undef PE_ACT8
+}
+// z to act(z), and d its slope
+__device__ __forceinline__ void act_both8(int act, float (&z)[8], float (&d)[8]) {
+#define PE_ACT8(A)                                              \
+    case A:                                                     \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) z[i] = act_both(A, z[i], d[i]); \
+        break
+    switch (act) {
+        PE_ACT8(PE_ACT_SILU);
+        PE_ACT8(PE_ACT_GELU);
+        PE_ACT8(PE_ACT_GELU_TANH);
+        PE_ACT8(PE_ACT_RELU);
+        default: _Pragma("unroll") for (int i = 0; i < 8; ++i) d[i] = 1.f;
+    }
+#undef PE_ACT8
+}
+
+template <typename E>
+__device__ __forceinline__ void unpack8(int4 r, float (&v)[8]) {
+    const uint32_t w[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = Elem<E>::unpack(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// The epilogue works on eight consecutive columns of a row: epi_cols loads
+// what all rows of these columns share, epi_load what the epilogue reads of
+// one row (ahead of its use, several rows at a time), epi_store finishes.
+// Rows and columns past the result load zeros and store nothing.
+struct EpiIn {
+    int4 a, b;
+};
+
+// bias of columns col..col+7
 template <typename E, int KIND>
-__device__ __forceinline__ void epilogue8(const Epi& e, int row, int col, float (&v)[8], const float (&u)[8]) {
+__device__ __forceinline__ void epi_cols(const Epi& e, int col, float (&bias)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias[i] = 0.f;
+    if (KIND == EPI_LINEAR && e.bias && col < e.cols)
+        load8(static_cast<const E*>(e.bias) + col, e.vec != 0, e.cols - col, bias);
+}
+template <typename E, int KIND>
+__device__ __forceinline__ EpiIn epi_load(const Epi& e, int row, int col) {
+    EpiIn in;
+    in.a = in.b = make_int4(0, 0, 0, 0);
+    if (row >= e.rows || col >= e.cols) return in;
+    if (KIND == EPI_LINEAR) {
+        if (e.res && e.vec) in.a = *reinterpret_cast<const int4*>(static_cast<const E*>(e.res) + row * e.ld_res + col);
+    } else if (KIND == EPI_GATED_BWD) {
+        const E* p = static_cast<const E*>(e.gu) + row * e.ld_keep + col;
+        in.a = *reinterpret_cast<const int4*>(p);
+        in.b = *reinterpret_cast<const int4*>(p + e.cols);
+    }
+    return in;
+}
+// v: the accumulators (of gate for EPI_GATED, where u holds up's; of dh for
+// EPI_GATED_BWD).  The one rounding to 16 bits is at each store.
+template <typename E, int KIND>
+__device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const float (&bias)[8], const EpiIn& in,
+                                          float (&v)[8], const float (&u)[8]) {
     const int n = e.cols - col;
     if (row >= e.rows || n <= 0) return;
-    const bool vec = e.vec != 0;  // cols % 8 = 0: all eight exist
     if (KIND == EPI_LINEAR) {
-        if (e.bias) {
-            float b[8];
-            load8(static_cast<const E*>(e.bias) + col, vec, n, b);
+        const bool vec = e.vec != 0;  // cols % 8 = 0: all eight exist
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += b[i];
-        }
+        for (int i = 0; i < 8; ++i) v[i] += bias[i];
         if (e.keep) store8(static_cast<E*>(e.keep) + row * e.ld_keep + col, vec, n, v);
-        if (e.act != PE_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = act_fwd(e.act, v[i]);
-        }
+        act_fwd8(e.act, v);
         if (e.res) {
             float r[8];
-            load8(static_cast<const E*>(e.res) + row * e.ld_res + col, vec, n, r);
+            if (vec) unpack8<E>(in.a, r);
+            else load8(static_cast<const E*>(e.res) + row * e.ld_res + col, false, n, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += r[i];
         }
         if (e.out_f32) store8_f32(static_cast<float*>(e.out) + row * e.ld_out + col, vec, n, v);
         else store8(static_cast<E*>(e.out) + row * e.ld_out + col, vec, n, v);
-    } else if (KIND == EPI_GATED) {
+    } else if (KIND == EPI_GATED) {  // cols is a multiple of 8 from here on
         if (e.keep) {
             E* k = static_cast<E*>(e.keep) + row * e.ld_keep + col;
-            store8(k, vec, n, v);
-            store8(k + e.cols, vec, n, u);
+            store8(k, true, 8, v);
+            store8(k + e.cols, true, 8, u);
         }
+        act_fwd8(e.act, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_fwd(e.act, v[i]) * u[i];
-        store8(static_cast<E*>(e.out) + row * e.ld_out + col, vec, n, v);
+        for (int i = 0; i < 8; ++i) v[i] *= u[i];
+        store8(static_cast<E*>(e.out) + row * e.ld_out + col, true, 8, v);
     } else {
-        const E* p = static_cast<const E*>(e.gu) + row * e.ld_keep + col;
-        float g[8], w[8];
-        load8(p, vec, n, g);
-        load8(p + e.cols, vec, n, w);
-        float dg[8], du[8], h[8];
+        float a[8], d[8], w[8];
+        unpack8<E>(in.a, a);
+        unpack8<E>(in.b, w);
+        act_both8(e.act, a, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float d;
-            const float a = act_both(e.act, g[i], d);
-            dg[i] = v[i] * w[i] * d;
-            du[i] = v[i] * a;
-            h[i] = a * w[i];
+            d[i] *= v[i] * w[i];  // dg
+            w[i] *= a[i];         // h
+            a[i] *= v[i];         // du
         }
         E* o = static_cast<E*>(e.out) + row * e.ld_out + col;
-        store8(o, vec, n, dg);
-        store8(o + e.cols, vec, n, du);
-        if (e.h) store8(static_cast<E*>(e.h) + row * (int64_t)e.cols + col, vec, n, h);
+        store8(o, true, 8, d);
+        store8(o + e.cols, true, 8, a);
+        if (e.h) store8(static_cast<E*>(e.h) + row * (int64_t)e.cols + col, true, 8, w);
     }
 }
 

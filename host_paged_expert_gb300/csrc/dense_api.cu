@@ -160,7 +160,7 @@ extern "C" pe_status pe_linear(const void* x, int64_t x_stride, const float* x_s
     p.e.ld_res = residual_stride;
     p.e.keep = keep;
     p.e.ld_keep = out_features;
-    return done(launch_product(p, EPI_LINEAR, elem, err, static_cast<cudaStream_t>(stream)));
+    return done(launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -229,13 +229,13 @@ extern "C" pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const
         Product p = make(dz, ld_dz, 0, weight, in_features, 1, rows, in_features, out_features);
         p.e.out = dx;
         p.e.ld_out = in_features;
-        e = launch_product(p, EPI_LINEAR, elem, err, st);
+        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
     }
     if (!e && dweight) {
         Product p = make(dz, ld_dz, 1, x, x_stride, 1, out_features, in_features, rows);
         p.e.out = dweight;
         p.e.ld_out = in_features;
-        e = launch_product(p, EPI_LINEAR, elem, err, st);
+        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
     }
     return done(e);
 }
@@ -272,7 +272,7 @@ extern "C" pe_status pe_gated_ffn(const void* x, int64_t x_stride, const void* w
         p.e.ld_out = intermediate;
         p.e.keep = keep;
         p.e.ld_keep = 2 * (int64_t)intermediate;
-        e = launch_product(p, EPI_GATED, elem, err, st);
+        e = launch_product(p, EPI_GATED, elem, CHAIN_BEFORE, err, st);
     }
     if (!e) {
         Product p = make(workspace, intermediate, 0, w2, intermediate, 0, rows, hidden, intermediate);
@@ -280,7 +280,7 @@ extern "C" pe_status pe_gated_ffn(const void* x, int64_t x_stride, const void* w
         p.e.ld_out = hidden;
         p.e.res = residual;
         p.e.ld_res = residual_stride;
-        e = launch_product(p, EPI_LINEAR, elem, err, st);
+        e = launch_product(p, EPI_LINEAR, elem, CHAIN_AFTER, err, st);
     }
     return done(e);
 }
@@ -329,25 +329,25 @@ extern "C" pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, co
         p.e.out = dgu;
         p.e.ld_out = I2;
         p.e.h = dw2 ? h : nullptr;
-        e = launch_product(p, EPI_GATED_BWD, elem, err, st);
+        e = launch_product(p, EPI_GATED_BWD, elem, CHAIN_NONE, err, st);
     }
     if (!e && dx) {
         Product p = make(dgu, I2, 0, w13, hidden, 1, rows, hidden, (int)I2);
         p.e.out = dx;
         p.e.ld_out = hidden;
-        e = launch_product(p, EPI_LINEAR, elem, err, st);
+        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
     }
     if (!e && dw13) {
         Product p = make(dgu, I2, 1, x, x_stride, 1, (int)I2, hidden, rows);
         p.e.out = dw13;
         p.e.ld_out = hidden;
-        e = launch_product(p, EPI_LINEAR, elem, err, st);
+        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
     }
     if (!e && dw2) {
         Product p = make(dy, dy_stride, 1, h, intermediate, 1, hidden, intermediate, rows);
         p.e.out = dw2;
         p.e.ld_out = intermediate;
-        e = launch_product(p, EPI_LINEAR, elem, err, st);
+        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
     }
     return done(e);
 }

@@ -29,8 +29,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 
@@ -41,6 +40,15 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, uint32
         if (mbar_try_wait(bar, parity)) return true;
     atomicOr(err, (uint32_t)PE_DEVERR_TIMEOUT);
     return false;
+}
+
+// One lane of a converged warp.  The loops that feed the tensor core are run
+// by whole warps with warp-uniform values, and only the issue is left to this
+// lane: descriptors then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 
 // Loads a box into this CTA's shared memory; the bytes count on `bar`, a

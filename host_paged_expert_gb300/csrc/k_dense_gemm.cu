@@ -32,21 +32,26 @@ PFN_encode encode_fn();
 namespace {
 
 constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 2 TMEM, 4..11 epilogue
-constexpr int kTile = 256;             // rows and columns of C per CTA pair
-constexpr int kHalf = 128;             // operand rows per CTA
-constexpr int kOperand = kHalf * 128;  // bytes of one operand's stage
-constexpr int kStage = 2 * kOperand;
+constexpr int kTile = 256;             // rows of C per CTA pair
+constexpr int kHalf = 128;             // of which each CTA has these
+constexpr int kOperand = kHalf * 128;  // bytes of A's stage in one CTA
 constexpr int kRaster = 8;             // tile rows walked together, so that their B tiles are shared in L2
+constexpr int kMaxStages = 8;
 
+// TN: columns of C per pair (of gate and up together), 256 or 128.
 constexpr int patch_bytes(int kind) { return kind == EPI_GATED ? 8192 : 4096; }
-constexpr int stages(int kind) { return kind == EPI_GATED ? 5 : 6; }
-constexpr int smem_bytes(int kind) { return 1024 + stages(kind) * kStage + 8 * patch_bytes(kind); }
+constexpr int stage_bytes(int tn) { return kOperand + tn / 2 * 128; }
+constexpr int stages(int kind, int tn) {
+    const int n = (225 * 1024 - 8 * patch_bytes(kind)) / stage_bytes(tn);
+    return n < kMaxStages ? n : kMaxStages;
+}
+constexpr int smem_bytes(int kind, int tn) { return 1024 + stages(kind, tn) * stage_bytes(tn) + 8 * patch_bytes(kind); }
 
 // Registers: 128 x (72 + 2 x 216) = 384 x 168, what the block is launched with.
 constexpr int kRegsFew = 72, kRegsMany = 216;
 
 struct Shared {
-    uint64_t full[6], empty[6], acc_full[2], acc_empty[2], drain;
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
 };
 
@@ -65,15 +70,35 @@ __device__ __forceinline__ void patch_get(const uint8_t* patch, int r, int c8, f
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
+// What the epilogue of a warp's 32 x 32 block reads, asked for before the
+// block's accumulators are there.
 template <typename E, int KIND>
-__device__ __forceinline__ void patch_out(const Epi& e, uint8_t* patch, int lane, int row0, int col0) {
+struct Ahead {
+    float bias[8];
+    EpiIn in[4];
+    __device__ __forceinline__ void load(const Epi& e, int lane, int row0, int col0) {
+        const int col = col0 + 8 * (lane & 3);
+        epi_cols<E, KIND>(e, col, bias);
 #pragma unroll
+        for (int it = 0; it < 4; ++it) in[it] = epi_load<E, KIND>(e, row0 + it * 8 + (lane >> 2), col);
+    }
+};
+
+// One round's code for all four: unrolled, the epilogue of one tile would
+// be 50 KB of instructions that a single-wave launch fetches cold (20.9
+// instead of 15 us at 256 x 2048 x 2048).
+template <typename E, int KIND>
+__device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, int lane, int row0, int col0,
+                                          const Ahead<E, KIND>& x) {
+    const int c8 = lane & 3;
+#pragma unroll 1
     for (int it = 0; it < 4; ++it) {
-        const int r = it * 8 + (lane >> 2), c8 = lane & 3;
+        const int r = it * 8 + (lane >> 2);
         float v[8], u[8];
         patch_get(patch, r, c8, v);
         if (KIND == EPI_GATED) patch_get(patch + 4096, r, c8, u);
-        epilogue8<E, KIND>(e, row0 + r, col0 + 8 * c8, v, u);
+        const EpiIn in = it == 0 ? x.in[0] : it == 1 ? x.in[1] : it == 2 ? x.in[2] : x.in[3];
+        epi_store<E, KIND>(e, row0 + r, col0 + 8 * c8, x.bias, in, v, u);
     }
 }
 
@@ -86,13 +111,13 @@ struct Tiles {
     }
 };
 
-template <typename E, int KIND, bool FP8>
+template <typename E, int KIND, bool FP8, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const __grid_constant__ Product p, uint32_t* err) {
-    constexpr int STAGES = stages(KIND);
+    constexpr int STAGES = stages(KIND, TN), kStage = stage_bytes(TN);
     constexpr int BK = FP8 ? 128 : 64;                      // elements of a 128-byte row
-    constexpr int NT = KIND == EPI_GATED ? kTile / 2 : kTile;  // result columns of a tile
+    constexpr int NT = KIND == EPI_GATED ? TN / 2 : TN;  // result columns of a tile
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -119,7 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::tma_prefetch(&ta);
         tc::tma_prefetch(&tb);
     }
-    if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 512);
+    if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 2 * TN);
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_arrive();
@@ -130,73 +155,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         if (FP8) tc::reg_dec<kRegsFew>();
-    if (warp == 0 && lane == 0) {
-        // ---- producer
-        uint32_t pos = 0;
-        bool ok = true;
-        for (int t = pair; t < tiles.total && ok; t += pairs) {
-            int mt, nt;
-            tiles.at(t, mt, nt);
-            const int m0 = mt * kTile + (int)rank * kHalf;
-            const int n0 = KIND == EPI_GATED ? (int)rank * p.e.cols + nt * NT : nt * NT + (int)rank * kHalf;
-            for (int kb = 0; kb < kblocks; ++kb, ++pos) {
-                const uint32_t s = pos % STAGES, use = pos / STAGES;
-                if (!(ok = tc::mbar_spin(&S.empty[s], (use & 1) ^ 1, err))) break;
-                if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * kStage);
-                const uint32_t bar = tc::map_rank(tc::smem_u32(&S.full[s]), 0);
-                uint8_t* a = ring + s * kStage;
-                uint8_t* b = a + kOperand;
-                if (p.a_mn) {
-                    tc::tma_load_2d_pair(a, &ta, bar, m0, kb * BK);
-                    tc::tma_load_2d_pair(a + 8192, &ta, bar, m0 + 64, kb * BK);
-                } else {
-                    tc::tma_load_2d_pair(a, &ta, bar, kb * BK, m0);
-                }
-                if (p.b_mn) {
-                    tc::tma_load_2d_pair(b, &tb, bar, n0, kb * BK);
-                    tc::tma_load_2d_pair(b + 8192, &tb, bar, n0 + 64, kb * BK);
-                } else {
-                    tc::tma_load_2d_pair(b, &tb, bar, kb * BK, n0);
+        if (warp == 0) {
+            // ---- producer
+            const bool lead = tc::elect_one();
+            const uint32_t bar0 = tc::map_rank(tc::smem_u32(&S.full[0]), 0);  // the leader's
+            uint32_t s = 0, phase = 1, issued = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles.total && ok; t += pairs) {
+                int mt, nt;
+                tiles.at(t, mt, nt);
+                const int m0 = mt * kTile + (int)rank * kHalf;
+                const int n0 = KIND == EPI_GATED ? (int)rank * p.e.cols + nt * NT : nt * NT + (int)rank * (TN / 2);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!(ok = tc::mbar_spin(&S.empty[s], phase, err))) break;
+                    if (lead) {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * kStage);
+                        const uint32_t bar = bar0 + 8 * s;
+                        uint8_t* a = ring + s * kStage;
+                        uint8_t* b = a + kOperand;
+                        if (p.a_mn) {
+                            tc::tma_load_2d_pair(a, &ta, bar, m0, kb * BK);
+                            tc::tma_load_2d_pair(a + 8192, &ta, bar, m0 + 64, kb * BK);
+                        } else {
+                            tc::tma_load_2d_pair(a, &ta, bar, kb * BK, m0);
+                        }
+                        if (p.b_mn) {
+                            tc::tma_load_2d_pair(b, &tb, bar, n0, kb * BK);
+                            if (TN == 256) tc::tma_load_2d_pair(b + 8192, &tb, bar, n0 + 64, kb * BK);
+                        } else {
+                            tc::tma_load_2d_pair(b, &tb, bar, kb * BK, n0);
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++s == STAGES) s = 0, phase ^= 1;
                 }
             }
-        }
-        // after a wait gave up: let this pair's copies land before the block ends
-        if (!ok && rank == 0)
-            for (uint32_t i = pos > STAGES ? pos - STAGES : 0; i < pos; ++i)
-                tc::mbar_wait(&S.full[i % STAGES], (i / STAGES) & 1, err, PE_DEVERR_TIMEOUT, 1u << 16);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-        // ---- MMA issuer
-        constexpr int FMT = FP8 ? 0 : std::is_same<E, __nv_bfloat16>::value ? 1 : 0;
-        const uint32_t id = tc::idesc(FMT, p.a_mn, p.b_mn, kTile, kTile);
-        const uint32_t astep = p.a_mn ? 2048 : 32, bstep = p.b_mn ? 2048 : 32;
-        uint32_t pos = 0, use_acc = 0;
-        bool ok = true;
-        for (int t = pair; t < tiles.total && ok; t += pairs) {
-            for (int kb = 0; kb < kblocks; ++kb, ++pos) {
-                const uint32_t buf = use_acc & 1;
-                if (FP8 || kb == 0) {
-                    if (!(ok = tc::mbar_spin(&S.acc_empty[buf], ((use_acc >> 1) & 1) ^ 1, err))) break;
-                }
-                const uint32_t s = pos % STAGES;
-                if (!(ok = tc::mbar_spin(&S.full[s], (pos / STAGES) & 1, err))) break;
-                tc::fence_after_sync();
-                const uint32_t a = tc::smem_u32(ring + s * kStage), b = a + kOperand;
+            // after a wait gave up: let this pair's copies land before the block ends
+            if (!ok && rank == 0)
+                for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+                    tc::mbar_wait(&S.full[i % STAGES], (i / STAGES) & 1, err, PE_DEVERR_TIMEOUT, 1u << 16);
+        } else if (warp == 1 && rank == 0) {
+            // ---- MMA issuer
+            const bool lead = tc::elect_one();
+            constexpr int FMT = FP8 ? 0 : std::is_same<E, __nv_bfloat16>::value ? 1 : 0;
+            const uint32_t id = tc::idesc(FMT, p.a_mn, p.b_mn, kTile, TN);
+            const uint32_t astep = (p.a_mn ? 2048 : 32) >> 4, bstep = (p.b_mn ? 2048 : 32) >> 4;
+            const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), p.a_mn);
+            const uint64_t b0 = tc::operand_desc(tc::smem_u32(ring) + kOperand, p.b_mn);
+            uint32_t s = 0, phase = 0, buf = 0, buf_phase = 1;
+            bool ok = true;
+            for (int t = pair; t < tiles.total && ok; t += pairs) {
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if ((FP8 || kb == 0) && !(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err))) break;
+                    if (!(ok = tc::mbar_spin(&S.full[s], phase, err))) break;
+                    tc::fence_after_sync();
+                    const bool last = FP8 || kb == kblocks - 1;
+                    if (lead) {
+                        const uint64_t a = a0 + s * (kStage >> 4), b = b0 + s * (kStage >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tc::mma<true, FP8>(tmem + buf * kTile, tc::operand_desc(a + k * astep, p.a_mn),
-                                       tc::operand_desc(b + k * bstep, p.b_mn), id, (!FP8 && kb) || k);
-                tc::mma_commit_pair(&S.empty[s]);
-                if (FP8 || kb == kblocks - 1) {
-                    tc::mma_commit_pair(&S.acc_full[buf]);
-                    ++use_acc;
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma<true, FP8>(tmem + buf * TN, a + k * astep, b + k * bstep, id, (!FP8 && kb) || k);
+                        tc::mma_commit_pair(&S.empty[s]);
+                        if (last) tc::mma_commit_pair(&S.acc_full[buf]);
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) s = 0, phase ^= 1;
+                    if (last) {
+                        buf ^= 1;
+                        if (buf == 0) buf_phase ^= 1;
+                    }
                 }
             }
+            if (!ok) {  // the MMAs already issued read shared memory and write TMEM
+                if (lead) tc::mma_commit_pair(&S.drain);
+                tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, 1u << 16);
+            }
         }
-        if (!ok) {  // the MMAs already issued read shared memory and write TMEM
-            tc::mma_commit_pair(&S.drain);
-            tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, 1u << 16);
-        }
-    }
     } else {
         // ---- epilogue
         if (FP8) tc::reg_inc<kRegsMany>();
@@ -226,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t r[32];
-                        tc::tmem_ld32(lanes + buf * kTile + half * 128 + c * 32, r);
+                        tc::tmem_ld32(lanes + buf * TN + half * 128 + c * 32, r);
                         tc::tmem_ld_wait();
                         if (c == 3) {
                             tc::fence_before_sync();
@@ -245,33 +280,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     patch_put(patch, lane, r);
                     __syncwarp();
-                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + half * 128 + c * 32);
+                    Ahead<E, KIND> x;
+                    x.load(p.e, lane, row0, nt * NT + half * 128 + c * 32);
+                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + half * 128 + c * 32, x);
                 }
             } else {
                 const uint32_t buf = use_acc & 1;
+                Ahead<E, KIND> x;
+                x.load(p.e, lane, row0, nt * NT + half * (NT / 2));
                 if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
                 ++use_acc;
                 tc::fence_after_sync();
                 constexpr int CH = NT / 64;  // 32-column chunks of this warp's half
+                const int c0 = half * (NT / 2);
+                const uint32_t at = lanes + buf * TN + c0;
+                uint32_t r[32];
+                tc::tmem_ld32(at, r);
 #pragma unroll 1
                 for (int c = 0; c < CH; ++c) {
-                    const int col = half * (NT / 2) + c * 32;
-                    uint32_t r[32];
-                    tc::tmem_ld32(lanes + buf * kTile + col, r);
                     tc::tmem_ld_wait();
                     __syncwarp();  // the patch's last readers are done
                     patch_put(patch, lane, r);
                     if (KIND == EPI_GATED) {
-                        tc::tmem_ld32(lanes + buf * kTile + kTile / 2 + col, r);
+                        tc::tmem_ld32(at + TN / 2 + c * 32, r);
                         tc::tmem_ld_wait();
                         patch_put(patch + 4096, lane, r);
                     }
                     if (c == CH - 1) {
                         tc::fence_before_sync();
                         if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
+                    } else {  // the next chunk is on its way while this one is stored
+                        tc::tmem_ld32(at + (c + 1) * 32, r);
                     }
                     __syncwarp();
-                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + col);
+                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + c0 + c * 32, x);
+                    if (c + 1 < CH) x.load(p.e, lane, row0, nt * NT + c0 + (c + 1) * 32);
                 }
             }
         }
@@ -283,16 +326,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::cluster_arrive();
     tc::cluster_wait();
     tc::fence_after_sync();
-    if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
+    if (warp == 2) tc::tmem_dealloc_pair(tmem, 2 * TN);
 }
 
-bool encode(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8) {
+bool encode(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t es = fp8 ? 1 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)(mn ? rows : k), (cuuint64_t)(mn ? k : rows)};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
-    const cuuint32_t box[2] = {fp8 ? 128u : 64u, mn ? 64u : (cuuint32_t)kHalf};
+    const cuuint32_t box[2] = {fp8 ? 128u : 64u, mn ? 64u : (cuuint32_t)box_rows};
     const cuuint32_t step[2] = {1, 1};
     // the type only sizes the elements: nothing is converted on the way
     return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
@@ -301,19 +344,19 @@ bool encode(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool 
 }
 
 // Pairs that the device holds at once, looked up once per kernel.
-template <typename E, int KIND, bool FP8>
+template <typename E, int KIND, bool FP8, int TN>
 cudaError_t resident_pairs(int* out) {
     static std::atomic<int> known[64];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     int n = dev < 64 ? known[dev].load() : 0;
     if (!n) {
-        auto k = pair_kernel<E, KIND, FP8>;
-        if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND))) return e;
+        auto k = pair_kernel<E, KIND, FP8, TN>;
+        if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND, TN))) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem_bytes(KIND);
+        cfg.dynamicSmemBytes = smem_bytes(KIND, TN);
         if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) return e;
         if (n < 1) return cudaErrorLaunchOutOfResources;
         if (dev < 64) known[dev].store(n);
@@ -322,26 +365,29 @@ cudaError_t resident_pairs(int* out) {
     return cudaSuccess;
 }
 
-template <typename E, int KIND, bool FP8>
+template <typename E, int KIND, bool FP8, int TN>
 cudaError_t launch(const Product& p, uint32_t* err, cudaStream_t st) {
     CUtensorMap ta, tb;
-    if (!encode(&ta, p.a, p.lda, p.M, p.K, p.a_mn, FP8) || !encode(&tb, p.b, p.ldb, p.N, p.K, p.b_mn, FP8))
+    if (!encode(&ta, p.a, p.lda, p.M, p.K, p.a_mn, FP8, kHalf) || !encode(&tb, p.b, p.ldb, p.N, p.K, p.b_mn, FP8, TN / 2))
         return cudaErrorInvalidValue;
     int pairs = 0;
-    if (cudaError_t e = resident_pairs<E, KIND, FP8>(&pairs)) return e;
-    const long long nt = KIND == EPI_GATED ? kTile / 2 : kTile;
+    if (cudaError_t e = resident_pairs<E, KIND, FP8, TN>(&pairs)) return e;
+    const long long nt = KIND == EPI_GATED ? TN / 2 : TN;
     const long long tiles = (long long)((p.M + kTile - 1) / kTile) * ((p.e.cols + nt - 1) / nt);
     if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
     if (tiles < pairs) pairs = (int)tiles;
-    return launch_pdl(pair_kernel<E, KIND, FP8>, dim3(2 * pairs), dim3(kThreads), smem_bytes(KIND), st, ta, tb, p, err);
+    return launch_pdl(pair_kernel<E, KIND, FP8, TN>, dim3(2 * pairs), dim3(kThreads), smem_bytes(KIND, TN), st, ta, tb, p, err);
 }
 
 template <typename E>
-cudaError_t launch_kind(const Product& p, EpiKind kind, uint32_t* err, cudaStream_t st) {
-    if (p.a_scale) return launch<E, EPI_LINEAR, true>(p, err, st);
-    if (kind == EPI_LINEAR) return launch<E, EPI_LINEAR, false>(p, err, st);
-    if (kind == EPI_GATED) return launch<E, EPI_GATED, false>(p, err, st);
-    return launch<E, EPI_GATED_BWD, false>(p, err, st);
+cudaError_t launch_kind(const Product& p, EpiKind kind, int tn, uint32_t* err, cudaStream_t st) {
+    if (p.a_scale) return launch<E, EPI_LINEAR, true, 256>(p, err, st);
+    if (kind == EPI_LINEAR)
+        return tn == 256 ? launch<E, EPI_LINEAR, false, 256>(p, err, st) : launch<E, EPI_LINEAR, false, 128>(p, err, st);
+    if (kind == EPI_GATED)
+        return tn == 256 ? launch<E, EPI_GATED, false, 256>(p, err, st) : launch<E, EPI_GATED, false, 128>(p, err, st);
+    return tn == 256 ? launch<E, EPI_GATED_BWD, false, 256>(p, err, st)
+                     : launch<E, EPI_GATED_BWD, false, 128>(p, err, st);
 }
 
 }  // namespace
@@ -356,8 +402,9 @@ PFN_encode encode_fn() {
     return fn;
 }
 
-cudaError_t launch_product(const Product& p, EpiKind kind, int elem, uint32_t* err, cudaStream_t st) {
-    return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, err, st) : launch_kind<__half>(p, kind, err, st);
+cudaError_t launch_pairs(const Product& p, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st) {
+    return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, tn, err, st)
+                                : launch_kind<__half>(p, kind, tn, err, st);
 }
 
 }  // namespace dense
