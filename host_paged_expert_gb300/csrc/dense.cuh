@@ -234,35 +234,18 @@ __device__ __forceinline__ float act_both(int act, float z, float& d) {
     }
 }
 
-// act of eight values (one branch for all of them)
-__device__ __forceinline__ void act_fwd8(int act, float (&v)[8]) {
-#define PE_ACT8(A)                                              \
-    case A:                                                     \
-        _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = act_fwd(A, v[i]); \
-        break
+// f with the activation as a compile-time constant: callers put the choice
+// outside of their loops, whose code then holds one activation only (a loop
+// over all five costs more in fetched instructions than in arithmetic).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
-        PE_ACT8(PE_ACT_SILU);
-        PE_ACT8(PE_ACT_GELU);
-        PE_ACT8(PE_ACT_GELU_TANH);
-        PE_ACT8(PE_ACT_RELU);
-        default: break;
+        case PE_ACT_SILU: f(std::integral_constant<int, PE_ACT_SILU>{}); break;
+        case PE_ACT_GELU: f(std::integral_constant<int, PE_ACT_GELU>{}); break;
+        case PE_ACT_GELU_TANH: f(std::integral_constant<int, PE_ACT_GELU_TANH>{}); break;
+        case PE_ACT_RELU: f(std::integral_constant<int, PE_ACT_RELU>{}); break;
+        default: f(std::integral_constant<int, PE_ACT_NONE>{}); break;
     }
-#undef PE_ACT8
-}
-// z to act(z), and d its slope
-__device__ __forceinline__ void act_both8(int act, float (&z)[8], float (&d)[8]) {
-#define PE_ACT8(A)                                              \
-    case A:                                                     \
-        _Pragma("unroll") for (int i = 0; i < 8; ++i) z[i] = act_both(A, z[i], d[i]); \
-        break
-    switch (act) {
-        PE_ACT8(PE_ACT_SILU);
-        PE_ACT8(PE_ACT_GELU);
-        PE_ACT8(PE_ACT_GELU_TANH);
-        PE_ACT8(PE_ACT_RELU);
-        default: _Pragma("unroll") for (int i = 0; i < 8; ++i) d[i] = 1.f;
-    }
-#undef PE_ACT8
 }
 
 template <typename E>
@@ -283,6 +266,12 @@ __device__ __forceinline__ void unpack8(int4 r, float (&v)[8]) {
 struct EpiIn {
     int4 a, b;
 };
+
+// Whether the epilogue is at most a bias and a residual, in vectors.
+template <int KIND>
+__device__ __forceinline__ bool epi_light(const Epi& e) {
+    return KIND == EPI_LINEAR && e.vec && !e.keep && !e.out_f32 && e.act == PE_ACT_NONE;
+}
 
 // bias of columns col..col+7
 template <typename E, int KIND>
@@ -308,7 +297,7 @@ __device__ __forceinline__ EpiIn epi_load(const Epi& e, int row, int col) {
 }
 // v: the accumulators (of gate for EPI_GATED, where u holds up's; of dh for
 // EPI_GATED_BWD).  The one rounding to 16 bits is at each store.
-template <typename E, int KIND>
+template <typename E, int KIND, int ACT>
 __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const float (&bias)[8], const EpiIn& in,
                                           float (&v)[8], const float (&u)[8]) {
     const int n = e.cols - col;
@@ -318,7 +307,9 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += bias[i];
         if (e.keep) store8(static_cast<E*>(e.keep) + row * e.ld_keep + col, vec, n, v);
-        act_fwd8(e.act, v);
+        if (ACT != PE_ACT_NONE)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_fwd(ACT, v[i]);
         if (e.res) {
             float r[8];
             if (vec) unpack8<E>(in.a, r);
@@ -334,17 +325,16 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
             store8(k, true, 8, v);
             store8(k + e.cols, true, 8, u);
         }
-        act_fwd8(e.act, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= u[i];
+        for (int i = 0; i < 8; ++i) v[i] = act_fwd(ACT, v[i]) * u[i];
         store8(static_cast<E*>(e.out) + row * e.ld_out + col, true, 8, v);
     } else {
         float a[8], d[8], w[8];
         unpack8<E>(in.a, a);
         unpack8<E>(in.b, w);
-        act_both8(e.act, a, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            a[i] = act_both(ACT, a[i], d[i]);
             d[i] *= v[i] * w[i];  // dg
             w[i] *= a[i];         // h
             a[i] *= v[i];         // du

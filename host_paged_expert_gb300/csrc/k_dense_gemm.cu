@@ -84,22 +84,39 @@ struct Ahead {
     }
 };
 
-// One round's code for all four: unrolled, the epilogue of one tile would
-// be 50 KB of instructions that a single-wave launch fetches cold (20.9
-// instead of 15 us at 256 x 2048 x 2048).
 template <typename E, int KIND>
 __device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, int lane, int row0, int col0,
                                           const Ahead<E, KIND>& x) {
-    const int c8 = lane & 3;
-#pragma unroll 1
-    for (int it = 0; it < 4; ++it) {
-        const int r = it * 8 + (lane >> 2);
-        float v[8], u[8];
-        patch_get(patch, r, c8, v);
-        if (KIND == EPI_GATED) patch_get(patch + 4096, r, c8, u);
-        const EpiIn in = it == 0 ? x.in[0] : it == 1 ? x.in[1] : it == 2 ? x.in[2] : x.in[3];
-        epi_store<E, KIND>(e, row0 + r, col0 + 8 * c8, x.bias, in, v, u);
+    const int c8 = lane & 3, row = row0 + (lane >> 2), col = col0 + 8 * c8;
+    if (epi_light<KIND>(e)) {
+        E* out = static_cast<E*>(e.out) + row * e.ld_out + col;
+        if (col < e.cols)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                float v[8];
+                patch_get(patch, it * 8 + (lane >> 2), c8, v);
+                if (e.bias)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += x.bias[i];
+                if (e.res) {
+                    float r[8];
+                    unpack8<E>(x.in[it].a, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += r[i];
+                }
+                if (row + it * 8 < e.rows) store8(out + it * 8 * e.ld_out, true, 8, v);
+            }
+        return;
     }
+    with_act(e.act, [&](auto act) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            float v[8], u[8];
+            patch_get(patch, it * 8 + (lane >> 2), c8, v);
+            if (KIND == EPI_GATED) patch_get(patch + 4096, it * 8 + (lane >> 2), c8, u);
+            epi_store<E, KIND, decltype(act)::value>(e, row + it * 8, col, x.bias, x.in[it], v, u);
+        }
+    });
 }
 
 struct Tiles {
@@ -246,43 +263,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tiles.at(t, mt, nt);
             const int row0 = mt * kTile + (int)rank * kHalf + quarter * 32;
             if (FP8) {
-                float acc[128];
+                uint64_t acc[4][16];  // pairs of fp32
 #pragma unroll
-                for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c][i] = 0;
                 const int row = row0 + lane, nb = (nt * NT + half * 128) / kGroup;
                 const bool live = row < p.M && nt * NT + half * 128 < p.N;
                 const float* as = p.a_scale + (size_t)(live ? row : 0) * kblocks;
                 const float* bs = p.b_scale + (size_t)(live ? nb : 0) * kblocks;
-                for (int kb = 0; kb < kblocks; ++kb, ++use_acc) {
-                    const float sc = live ? __ldg(as + kb) * __ldg(bs + kb) : 0.f;
-                    const uint32_t buf = use_acc & 1;
+                float next = live ? __ldg(as) * __ldg(bs) : 0.f;
+                if (p.e.res && p.e.vec && live) {  // the residual's 256 bytes on their way to L2
+                    const uint8_t* rp = static_cast<const uint8_t*>(p.e.res) + 2 * (row * p.e.ld_res + nt * NT + half * 128);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (nt * NT + half * 128 + 64 * i < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + 128 * i));
+                }
+                for (int kb = 0; kb < kblocks && ok; ++kb) {
+                    const uint64_t sc = tc::pack2(__float_as_uint(next), __float_as_uint(next));
+                    if (kb + 1 < kblocks && live) next = __ldg(as + kb + 1) * __ldg(bs + kb + 1);
+                    const uint32_t buf = use_acc & 1, at = lanes + buf * TN + half * 128;
                     if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
                     tc::fence_after_sync();
+                    ++use_acc;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(lanes + buf * TN + half * 128 + c * 32, r);
+                    for (int h = 0; h < 2; ++h) {
+                        // 64 columns at once; the other warp of this scheduler adds while this one reads
+                        uint32_t r[2][32];
+                        tc::tmem_ld32(at + h * 64, r[0]);
+                        tc::tmem_ld32(at + h * 64 + 32, r[1]);
                         tc::tmem_ld_wait();
-                        if (c == 3) {
+                        if (h == 1) {
                             tc::fence_before_sync();
                             if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sc, acc[c * 32 + i]);
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                acc[2 * h + c][i] = tc::fma2(tc::pack2(r[c][2 * i], r[c][2 * i + 1]), sc, acc[2 * h + c][i]);
                     }
                 }
                 if (!ok) break;
+                const int col0 = nt * NT + half * 128;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c * 32 + i]);
-                    __syncwarp();
-                    patch_put(patch, lane, r);
-                    __syncwarp();
                     Ahead<E, KIND> x;
-                    x.load(p.e, lane, row0, nt * NT + half * 128 + c * 32);
-                    patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + half * 128 + c * 32, x);
+                    x.load(p.e, lane, row0, col0 + c * 32);
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) tc::unpack2(acc[c][i], o[2 * i], o[2 * i + 1]);
+                    __syncwarp();
+                    patch_put(patch, lane, o);
+                    __syncwarp();
+                    patch_out<E, KIND>(p.e, patch, lane, row0, col0 + c * 32, x);
                 }
             } else {
                 const uint32_t buf = use_acc & 1;
@@ -294,10 +328,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 constexpr int CH = NT / 64;  // 32-column chunks of this warp's half
                 const int c0 = half * (NT / 2);
                 const uint32_t at = lanes + buf * TN + c0;
-                uint32_t r[32];
-                tc::tmem_ld32(at, r);
 #pragma unroll 1
                 for (int c = 0; c < CH; ++c) {
+                    Ahead<E, KIND> n;
+                    if (c + 1 < CH) n.load(p.e, lane, row0, nt * NT + c0 + (c + 1) * 32);
+                    uint32_t r[32];
+                    tc::tmem_ld32(at + c * 32, r);
                     tc::tmem_ld_wait();
                     __syncwarp();  // the patch's last readers are done
                     patch_put(patch, lane, r);
@@ -309,12 +345,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (c == CH - 1) {
                         tc::fence_before_sync();
                         if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
-                    } else {  // the next chunk is on its way while this one is stored
-                        tc::tmem_ld32(at + (c + 1) * 32, r);
                     }
                     __syncwarp();
                     patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + c0 + c * 32, x);
-                    if (c + 1 < CH) x.load(p.e, lane, row0, nt * NT + c0 + (c + 1) * 32);
+                    x = n;
                 }
             }
         }

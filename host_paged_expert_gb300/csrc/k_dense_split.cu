@@ -104,24 +104,14 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
                     }
             }
         }
-        // one copy of the epilogue's code for all units
-#pragma unroll 1
-        for (int i = 0; i < BATCH; ++i) {
-            const int u = ub + i * kThreads;
-            if (u >= total) break;
-            float x[G][8];
-            EpiIn n = in[0];
+        with_act(e.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k)
-                if (k == i) {
-                    n = in[k];
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[g][j] = v[k][g][j];
-                }
-            epi_store<E, KIND>(e, t0 + r0 + u / U, col, bias, n, x[0], x[G - 1]);
-        }
+            for (int i = 0; i < BATCH; ++i) {
+                const int u = ub + i * kThreads;
+                if (u < total)
+                    epi_store<E, KIND, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0], v[i][G - 1]);
+            }
+        });
     }
 }
 
