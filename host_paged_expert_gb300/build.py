@@ -1,7 +1,8 @@
 """Build libpe.so in-tree with nvcc for GB300 (sm_103a).
 
 Every .cu file under csrc/ is compiled in parallel to an object file, then
-linked into ``host_paged_expert_gb300/libpe.so``.  Run as
+linked into ``host_paged_expert_gb300/libpe.so``; the Python binding of the
+dense operators (csrc/py_dense.c) becomes ``_dense.so`` next to it.  Run as
 ``python -m host_paged_expert_gb300.build`` or call ``build()``.
 """
 
@@ -13,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpe.so")
+PYEXT = os.path.join(PKG, "_dense.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}"]
@@ -57,7 +60,22 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     return LIB
+
+
+def _build_binding() -> None:
+    """Compile the CPython binding and link it against libpe.so beside it."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found")
+    tmp = PYEXT + ".tmp"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-Wall", "-Werror", f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(ROOT, 'include')}",
+           os.path.join(CSRC, "py_dense.c"), f"-L{PKG}", "-l:libpe.so", "-Wl,-rpath,$ORIGIN", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYEXT)
 
 
 if __name__ == "__main__":
