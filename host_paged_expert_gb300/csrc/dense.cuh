@@ -80,6 +80,9 @@ struct SplitShape {
 cudaError_t launch_pairs(const Product& p, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st);
 cudaError_t launch_split(const Product& p, EpiKind kind, int elem, const SplitShape& s, int chain, uint32_t* err,
                          cudaStream_t st);
+// Up to kGemvRows rows, forward products: weights streamed by warps, no tensor core.
+constexpr int kGemvRows = 4;
+cudaError_t launch_gemv(const Product& p, EpiKind kind, int elem, int chain, cudaStream_t st);
 // K blocks of 64 that one accumulator takes where the result is fp32, of kb in all.
 int split_blocks(const SplitShape& s, int kb);
 
@@ -343,6 +346,27 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
         store8(o, true, 8, d);
         store8(o + e.cols, true, 8, a);
         if (e.h) store8(static_cast<E*>(e.h) + row * (int64_t)e.cols + col, true, 8, w);
+    }
+}
+
+// The same for a single element (EPI_LINEAR, EPI_GATED).
+template <typename E, int KIND>
+__device__ __forceinline__ void epi_store1(const Epi& e, int row, int col, float v, float u) {
+    if (row >= e.rows || col >= e.cols) return;
+    E* keep = static_cast<E*>(e.keep) + row * e.ld_keep + col;
+    if (KIND == EPI_LINEAR) {
+        if (e.bias) v += Elem<E>::get(static_cast<const E*>(e.bias)[col]);
+        if (e.keep) *keep = Elem<E>::put(v);
+        v = act_fwd(e.act, v);
+        if (e.res) v += Elem<E>::get(static_cast<const E*>(e.res)[row * e.ld_res + col]);
+        if (e.out_f32) static_cast<float*>(e.out)[row * e.ld_out + col] = v;
+        else static_cast<E*>(e.out)[row * e.ld_out + col] = Elem<E>::put(v);
+    } else {
+        if (e.keep) {
+            keep[0] = Elem<E>::put(v);
+            keep[e.cols] = Elem<E>::put(u);
+        }
+        static_cast<E*>(e.out)[row * e.ld_out + col] = Elem<E>::put(act_fwd(e.act, v) * u);
     }
 }
 

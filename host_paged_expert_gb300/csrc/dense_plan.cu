@@ -10,6 +10,14 @@
 //   512 x 8192 x 1024      42.3 / 31.4               37.0 (64, 1)  21.9 (64, 2)  17.9 (128, 4)
 //   1024 x 2048 x 2048     17.1 / 13.1               17.1 (64, 1)  21.9 (64, 2)  16.3 (128, 1)
 //   1024 x 4096 x 4096     26.6 / 32.8               49.3 (64, 1)
+//
+//   rows x K x cols   warps streaming weights        best cluster split
+//   1 x 4096 x 2048         2.7                       6.8
+//   1 x 8192 x 8192        18.6                      24.2
+//   2 x 4096 x 4096         6.2                       8.2
+//   4 x 2048 x 2048         4.0                       5.7
+//   4 x 8192 x 8192        40.4                      24.4
+//   8 x 2048 x 2048         8.1                       6.1
 #include <algorithm>
 #include <cmath>
 
@@ -37,7 +45,7 @@ double pair_time(const Product& p, EpiKind kind, int tn) {
     return fixed + full * std::min(1.0, p.M / 256.0) + waves * kb * block + (waves - 1) * std::max(0.0, epi - kb * block);
 }
 
-// The same with the K blocks of one CTA; blocks on one SM share its tensor
+// The same with the K blocks of one CTA (or all weights from HBM); blocks on one SM share its tensor
 // core; partial sums cross the cluster at about 1.6 TB/s.
 double split_time(const Product& p, EpiKind kind, const SplitShape& s) {
     const bool fp8 = p.a_scale != nullptr;
@@ -46,8 +54,16 @@ double split_time(const Product& p, EpiKind kind, const SplitShape& s) {
     const double block = fp8 ? 0.26 + 0.0045 * s.nt : s.nt <= 64 ? 0.245 : 0.275;
     const double slots = s.nt <= 64 ? 2 * kSms : kSms;
     const double fixed = 3.6 + 0.0245 * s.nt, waves = std::max(1.0, std::ceil(ctas / slots));
-    return fixed * waves + share * block * std::max(1.0, ctas / kSms) +
+    const double stream = (double)p.N * p.K * (fp8 ? 1 : 2) / 6.2e6;  // the weights at HBM's rate
+    return fixed * waves + std::max(stream, share * block * std::max(1.0, ctas / kSms)) +
            base * s.nt * 512.0 * (s.split - 1) / 1.6e6 + 0.1 * (s.split - 1);
+}
+
+// Weights at what HBM and L2 gave, or the multiply-adds with operands from L1.
+double gemv_time(const Product& p) {
+    const bool fp8 = p.a_scale != nullptr;
+    const double weights = (double)p.N * p.K;
+    return 1.7 + std::max(weights * (fp8 ? 1 : 2) / 7.2e6, p.M * weights / (fp8 ? 5.0e6 : 6.3e6));
 }
 
 }  // namespace
@@ -76,6 +92,8 @@ cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, 
             if (fits > bounded || (fits == bounded && us < best)) best = us, tn = 0, shape = s, bounded = fits;
         }
     }
+    if (p.M <= kGemvRows && !p.a_mn && !p.b_mn && kind != EPI_GATED_BWD && gemv_time(p) < best)
+        return launch_gemv(p, kind, elem, chain, st);
     if (tn) return launch_pairs(p, kind, elem, tn, err, st);
     return launch_split(p, kind, elem, shape, chain, err, st);
 }
