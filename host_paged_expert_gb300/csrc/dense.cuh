@@ -71,13 +71,18 @@ enum { CHAIN_NONE = 0, CHAIN_BEFORE = 1, CHAIN_AFTER = 2 };
 // elem: pe_elem of the 16-bit operands and of every 16-bit tensor of the epilogue.
 cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, uint32_t* err, cudaStream_t st);
 
-// The two kernels behind launch_product: tiles of 256 rows x tn (256 or 128)
+// Independent EPI_LINEAR products of 16-bit results, in any order or all at once.
+cudaError_t launch_products(const Product* p, int count, int elem, uint32_t* err, cudaStream_t st);
+
+// The kernels behind launch_product: tiles of 256 rows x tn (256 or 128)
 // columns on CTA pairs, and tiles of 128 columns x nt rows whose K axis a
 // cluster of `split` CTAs shares.
 struct SplitShape {
     int nt, split;
 };
-cudaError_t launch_pairs(const Product& p, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st);
+// launch_pairs: up to kMostProducts EPI_LINEAR products of 16-bit operands in one launch, else one.
+constexpr int kMostProducts = 3;
+cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st);
 cudaError_t launch_split(const Product& p, EpiKind kind, int elem, const SplitShape& s, int chain, uint32_t* err,
                          cudaStream_t st);
 // Up to kGemvRows rows, forward products: weights streamed by warps, no tensor core.

@@ -225,18 +225,19 @@ extern "C" pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const
         a.cols = out_features;
         e = launch_act_bwd(a, elem, st);
     }
-    if (!e && dx) {
-        Product p = make(dz, ld_dz, 0, weight, in_features, 1, rows, in_features, out_features);
-        p.e.out = dx;
-        p.e.ld_out = in_features;
-        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
+    Product p[2];
+    int n = 0;
+    if (dx) {
+        p[n] = make(dz, ld_dz, 0, weight, in_features, 1, rows, in_features, out_features);
+        p[n].e.out = dx;
+        p[n++].e.ld_out = in_features;
     }
-    if (!e && dweight) {
-        Product p = make(dz, ld_dz, 1, x, x_stride, 1, out_features, in_features, rows);
-        p.e.out = dweight;
-        p.e.ld_out = in_features;
-        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
+    if (dweight) {
+        p[n] = make(dz, ld_dz, 1, x, x_stride, 1, out_features, in_features, rows);
+        p[n].e.out = dweight;
+        p[n++].e.ld_out = in_features;
     }
+    if (!e) e = launch_products(p, n, elem, err, st);
     return done(e);
 }
 
@@ -331,23 +332,23 @@ extern "C" pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, co
         p.e.h = dw2 ? h : nullptr;
         e = launch_product(p, EPI_GATED_BWD, elem, CHAIN_NONE, err, st);
     }
-    if (!e && dx) {
-        Product p = make(dgu, I2, 0, w13, hidden, 1, rows, hidden, (int)I2);
-        p.e.out = dx;
-        p.e.ld_out = hidden;
-        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
+    Product p[3];
+    int n = 0;
+    if (dx) {
+        p[n] = make(dgu, I2, 0, w13, hidden, 1, rows, hidden, (int)I2);
+        p[n].e.out = dx;
+        p[n++].e.ld_out = hidden;
     }
-    if (!e && dw13) {
-        Product p = make(dgu, I2, 1, x, x_stride, 1, (int)I2, hidden, rows);
-        p.e.out = dw13;
-        p.e.ld_out = hidden;
-        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
+    if (dw13) {
+        p[n] = make(dgu, I2, 1, x, x_stride, 1, (int)I2, hidden, rows);
+        p[n].e.out = dw13;
+        p[n++].e.ld_out = hidden;
     }
-    if (!e && dw2) {
-        Product p = make(dy, dy_stride, 1, h, intermediate, 1, hidden, intermediate, rows);
-        p.e.out = dw2;
-        p.e.ld_out = intermediate;
-        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
+    if (dw2) {
+        p[n] = make(dy, dy_stride, 1, h, intermediate, 1, hidden, intermediate, rows);
+        p[n].e.out = dw2;
+        p[n++].e.ld_out = intermediate;
     }
+    if (!e) e = launch_products(p, n, elem, err, st);
     return done(e);
 }

@@ -66,19 +66,23 @@ double gemv_time(const Product& p) {
     return 1.7 + std::max(weights * (fp8 ? 1 : 2) / 7.2e6, p.M * weights / (fp8 ? 5.0e6 : 6.3e6));
 }
 
-}  // namespace
+// The best kernel for one product and its time.
+struct Choice {
+    double us = 1e30;
+    int tn = 0;            // CTA pairs with tiles of so many columns
+    bool gemv = false;
+    SplitShape shape = {};  // else a cluster split
+};
 
-cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, uint32_t* err, cudaStream_t st) {
+Choice choose(const Product& p, EpiKind kind) {
     const bool fp8 = p.a_scale != nullptr, f32 = p.e.out_f32 != 0;
     const int kb = up(p.K, fp8 ? 128 : 64);
-    double best = 1e30;
-    int tn = 0;
-    SplitShape shape = {};
+    Choice c;
     // fp32 results stay with the kernel that bounds the terms of one accumulator
     if (!f32 || fp8)
         for (int t = 256; t >= (fp8 ? 256 : 128); t /= 2) {
             const double us = pair_time(p, kind, t);
-            if (us < best) best = us, tn = t;
+            if (us < c.us) c.us = us, c.tn = t;
         }
     bool bounded = !f32 || fp8;  // whether the best shape keeps its accumulators to 8 blocks, where that matters
     for (int most = 32; most <= (fp8 ? 64 : 128); most *= 2) {
@@ -89,13 +93,62 @@ cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, 
         for (s.split = 1; s.split <= 8 && s.split <= kb; s.split *= 2) {
             const double us = split_time(p, kind, s);
             const bool fits = !f32 || fp8 || split_blocks(s, kb) <= 8;
-            if (fits > bounded || (fits == bounded && us < best)) best = us, tn = 0, shape = s, bounded = fits;
+            if (fits > bounded || (fits == bounded && us < c.us)) c.us = us, c.tn = 0, c.shape = s, bounded = fits;
         }
     }
-    if (p.M <= kGemvRows && !p.a_mn && !p.b_mn && kind != EPI_GATED_BWD && gemv_time(p) < best)
-        return launch_gemv(p, kind, elem, chain, st);
-    if (tn) return launch_pairs(p, kind, elem, tn, err, st);
-    return launch_split(p, kind, elem, shape, chain, err, st);
+    if (p.M <= kGemvRows && !p.a_mn && !p.b_mn && kind != EPI_GATED_BWD) {
+        const double us = gemv_time(p);
+        if (us < c.us) c.us = us, c.gemv = true;
+    }
+    return c;
+}
+
+cudaError_t launch_choice(const Choice& c, const Product& p, EpiKind kind, int elem, int chain, uint32_t* err,
+                          cudaStream_t st) {
+    if (c.gemv) return launch_gemv(p, kind, elem, chain, st);
+    if (c.tn) return launch_pairs(&p, 1, kind, elem, c.tn, err, st);
+    return launch_split(p, kind, elem, c.shape, chain, err, st);
+}
+
+// Products of 16-bit operands in one launch: the pair with the most K blocks.
+double group_time(const Product* p, int count, int tn) {
+    double load[(int)kPairs] = {};
+    long long t = 0;
+    for (int i = 0; i < count; ++i) {
+        const long long n = (long long)up(p[i].M, 256) * up(p[i].e.cols, tn);
+        const double kb = up(p[i].K, 64), whole = (double)(n / (int)kPairs) * kb;
+        for (int j = 0; j < (int)kPairs; ++j)
+            load[j] += whole + (((j - t) % (int)kPairs + (int)kPairs) % (int)kPairs < n % (int)kPairs ? kb : 0);
+        t += n;
+    }
+    const double most = *std::max_element(load, load + (int)kPairs);
+    return (tn == 256 ? 8.6 : 6.3) + most * (tn == 256 ? 0.265 : 0.195);
+}
+
+}  // namespace
+
+cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, uint32_t* err, cudaStream_t st) {
+    return launch_choice(choose(p, kind), p, kind, elem, chain, err, st);
+}
+
+cudaError_t launch_products(const Product* p, int count, int elem, uint32_t* err, cudaStream_t st) {
+    if (count > kMostProducts) return cudaErrorInvalidValue;
+    Choice c[kMostProducts];
+    Product by_k[kMostProducts];  // the longest tiles first
+    double apart = 0;
+    for (int i = 0; i < count; ++i) {
+        c[i] = choose(p[i], EPI_LINEAR);
+        apart += c[i].us;
+        by_k[i] = p[i];
+    }
+    std::sort(by_k, by_k + count, [](const Product& a, const Product& b) { return a.K > b.K; });
+    if (count > 1)
+        for (int tn = 256; tn >= 128; tn /= 2)
+            if (group_time(by_k, count, tn) < apart && group_time(by_k, count, tn) <= group_time(by_k, count, 384 - tn))
+                return launch_pairs(by_k, count, EPI_LINEAR, elem, tn, err, st);
+    for (int i = 0; i < count; ++i)
+        if (cudaError_t e = launch_choice(c[i], p[i], EPI_LINEAR, elem, CHAIN_NONE, err, st)) return e;
+    return cudaSuccess;
 }
 
 }  // namespace dense

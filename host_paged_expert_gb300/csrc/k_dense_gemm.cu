@@ -119,19 +119,40 @@ __device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, in
     });
 }
 
-struct Tiles {
-    int tm, tn, total;
-    __device__ __forceinline__ void at(int t, int& m, int& n) const {
-        const int per = kRaster * tn, first = t / per * kRaster, rows = min(kRaster, tm - first), r = t % per;
+// Products that one launch computes: their tiles are dealt out to the pairs
+// as one sequence, so that a product's last wave is filled by the next one's
+// tiles.
+template <int N>
+struct Work {
+    CUtensorMap a[N], b[N];
+    Product p[N];
+    int tiles[N];
+    int count;
+};
+
+// A pair's way through them: tiles pair, pair + pairs, ...
+struct Walk {
+    int t, i = 0, base = 0;
+    template <int N>
+    __device__ __forceinline__ bool find(const Work<N>& w) {
+        if (N == 1) return t < w.tiles[0];
+        while (i < w.count && t - base >= w.tiles[i]) base += w.tiles[i++];
+        return i < w.count;
+    }
+    // row and column of the tile in its product: kRaster tile rows at a time
+    __device__ __forceinline__ void at(const Product& p, int cols, int& m, int& n) const {
+        const int tm = (p.M + kTile - 1) / kTile, tn = (p.e.cols + cols - 1) / cols;
+        const int per = kRaster * tn, first = (t - base) / per * kRaster, rows = min(kRaster, tm - first), r = (t - base) % per;
         m = first + r % rows;
         n = r / rows;
     }
 };
 
-template <typename E, int KIND, bool FP8, int TN>
+// NP: products that the launch may hold.  With one, its fields are constants
+// of the instructions; found by index they cost 5 % of a large product's time.
+template <typename E, int KIND, bool FP8, int TN, int NP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                const __grid_constant__ Product p, uint32_t* err) {
+    pair_kernel(const __grid_constant__ Work<NP> work, uint32_t* err) {
     constexpr int STAGES = stages(KIND, TN), kStage = stage_bytes(TN);
     constexpr int BK = FP8 ? 128 : 64;                      // elements of a 128-byte row
     constexpr int NT = KIND == EPI_GATED ? TN / 2 : TN;  // result columns of a tile
@@ -141,11 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    Tiles tiles;
-    tiles.tm = (p.M + kTile - 1) / kTile;
-    tiles.tn = (p.e.cols + NT - 1) / NT;
-    tiles.total = tiles.tm * tiles.tn;
-    const int kblocks = (p.K + BK - 1) / BK;
+    Walk walk{pair};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -158,8 +175,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc::mbar_init(&S.drain, 1);
         tc::fence_barrier_init();
-        tc::tma_prefetch(&ta);
-        tc::tma_prefetch(&tb);
+        tc::tma_prefetch(&work.a[0]);
+        tc::tma_prefetch(&work.b[0]);
     }
     if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 2 * TN);
     tc::fence_before_sync();
@@ -178,9 +195,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t bar0 = tc::map_rank(tc::smem_u32(&S.full[0]), 0);  // the leader's
             uint32_t s = 0, phase = 1, issued = 0;
             bool ok = true;
-            for (int t = pair; t < tiles.total && ok; t += pairs) {
+            for (; ok && walk.find(work); walk.t += pairs) {
+                const Product& p = work.p[NP == 1 ? 0 : walk.i];
+                const CUtensorMap &ta = work.a[NP == 1 ? 0 : walk.i], &tb = work.b[NP == 1 ? 0 : walk.i];
+                const int kblocks = (p.K + BK - 1) / BK;
                 int mt, nt;
-                tiles.at(t, mt, nt);
+                walk.at(p, NT, mt, nt);
                 const int m0 = mt * kTile + (int)rank * kHalf;
                 const int n0 = KIND == EPI_GATED ? (int)rank * p.e.cols + nt * NT : nt * NT + (int)rank * (TN / 2);
                 for (int kb = 0; kb < kblocks; ++kb) {
@@ -216,13 +236,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // ---- MMA issuer
             const bool lead = tc::elect_one();
             constexpr int FMT = FP8 ? 0 : std::is_same<E, __nv_bfloat16>::value ? 1 : 0;
-            const uint32_t id = tc::idesc(FMT, p.a_mn, p.b_mn, kTile, TN);
-            const uint32_t astep = (p.a_mn ? 2048 : 32) >> 4, bstep = (p.b_mn ? 2048 : 32) >> 4;
-            const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), p.a_mn);
-            const uint64_t b0 = tc::operand_desc(tc::smem_u32(ring) + kOperand, p.b_mn);
             uint32_t s = 0, phase = 0, buf = 0, buf_phase = 1;
             bool ok = true;
-            for (int t = pair; t < tiles.total && ok; t += pairs) {
+            for (; ok && walk.find(work); walk.t += pairs) {
+                const Product& p = work.p[NP == 1 ? 0 : walk.i];
+                const int kblocks = (p.K + BK - 1) / BK;
+                const uint32_t id = tc::idesc(FMT, p.a_mn, p.b_mn, kTile, TN);
+                const uint32_t astep = (p.a_mn ? 2048 : 32) >> 4, bstep = (p.b_mn ? 2048 : 32) >> 4;
+                const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), p.a_mn);
+                const uint64_t b0 = tc::operand_desc(tc::smem_u32(ring) + kOperand, p.b_mn);
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if ((FP8 || kb == 0) && !(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err))) break;
                     if (!(ok = tc::mbar_spin(&S.full[s], phase, err))) break;
@@ -258,9 +280,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t release = tc::map_rank(tc::smem_u32(&S.acc_empty[0]), 0);  // of the pair's leader
         uint32_t use_acc = 0;
         bool ok = true;
-        for (int t = pair; t < tiles.total && ok; t += pairs) {
+        for (; ok && walk.find(work); walk.t += pairs) {
+            const Product& p = work.p[NP == 1 ? 0 : walk.i];
+            const int kblocks = (p.K + BK - 1) / BK;
             int mt, nt;
-            tiles.at(t, mt, nt);
+            walk.at(p, NT, mt, nt);
             const int row0 = mt * kTile + (int)rank * kHalf + quarter * 32;
             if (FP8) {
                 uint64_t acc[4][16];  // pairs of fp32
@@ -378,14 +402,14 @@ bool encode(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool 
 }
 
 // Pairs that the device holds at once, looked up once per kernel.
-template <typename E, int KIND, bool FP8, int TN>
+template <typename E, int KIND, bool FP8, int TN, int NP>
 cudaError_t resident_pairs(int* out) {
     static std::atomic<int> known[64];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     int n = dev < 64 ? known[dev].load() : 0;
     if (!n) {
-        auto k = pair_kernel<E, KIND, FP8, TN>;
+        auto k = pair_kernel<E, KIND, FP8, TN, NP>;
         if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND, TN))) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
@@ -399,29 +423,42 @@ cudaError_t resident_pairs(int* out) {
     return cudaSuccess;
 }
 
-template <typename E, int KIND, bool FP8, int TN>
-cudaError_t launch(const Product& p, uint32_t* err, cudaStream_t st) {
-    CUtensorMap ta, tb;
-    if (!encode(&ta, p.a, p.lda, p.M, p.K, p.a_mn, FP8, kHalf) || !encode(&tb, p.b, p.ldb, p.N, p.K, p.b_mn, FP8, TN / 2))
-        return cudaErrorInvalidValue;
+template <typename E, int KIND, bool FP8, int TN, int NP = 1>
+cudaError_t launch(const Product* p, int count, uint32_t* err, cudaStream_t st) {
+    if (count < 1 || count > NP) return cudaErrorInvalidValue;
+    Work<NP> w;
+    w.count = count;
+    long long tiles = 0;
+    for (int i = 0; i < count; ++i) {
+        if (!encode(&w.a[i], p[i].a, p[i].lda, p[i].M, p[i].K, p[i].a_mn, FP8, kHalf) ||
+            !encode(&w.b[i], p[i].b, p[i].ldb, p[i].N, p[i].K, p[i].b_mn, FP8, TN / 2))
+            return cudaErrorInvalidValue;
+        w.p[i] = p[i];
+        constexpr int NT = KIND == EPI_GATED ? TN / 2 : TN;
+        const long long n = (long long)((p[i].M + kTile - 1) / kTile) * ((p[i].e.cols + NT - 1) / NT);
+        if ((tiles += n) > INT_MAX / 2) return cudaErrorInvalidValue;
+        w.tiles[i] = (int)n;
+    }
     int pairs = 0;
-    if (cudaError_t e = resident_pairs<E, KIND, FP8, TN>(&pairs)) return e;
-    const long long nt = KIND == EPI_GATED ? TN / 2 : TN;
-    const long long tiles = (long long)((p.M + kTile - 1) / kTile) * ((p.e.cols + nt - 1) / nt);
-    if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
+    if (cudaError_t e = resident_pairs<E, KIND, FP8, TN, NP>(&pairs)) return e;
     if (tiles < pairs) pairs = (int)tiles;
-    return launch_pdl(pair_kernel<E, KIND, FP8, TN>, dim3(2 * pairs), dim3(kThreads), smem_bytes(KIND, TN), st, ta, tb, p, err);
+    return launch_pdl(pair_kernel<E, KIND, FP8, TN, NP>, dim3(2 * pairs), dim3(kThreads), smem_bytes(KIND, TN), st, w, err);
 }
 
 template <typename E>
-cudaError_t launch_kind(const Product& p, EpiKind kind, int tn, uint32_t* err, cudaStream_t st) {
-    if (p.a_scale) return launch<E, EPI_LINEAR, true, 256>(p, err, st);
+cudaError_t launch_kind(const Product* p, int count, EpiKind kind, int tn, uint32_t* err, cudaStream_t st) {
+    if (p->a_scale) return launch<E, EPI_LINEAR, true, 256>(p, count, err, st);
+    if (count > 1 && kind == EPI_LINEAR)
+        return tn == 256 ? launch<E, EPI_LINEAR, false, 256, kMostProducts>(p, count, err, st)
+                         : launch<E, EPI_LINEAR, false, 128, kMostProducts>(p, count, err, st);
     if (kind == EPI_LINEAR)
-        return tn == 256 ? launch<E, EPI_LINEAR, false, 256>(p, err, st) : launch<E, EPI_LINEAR, false, 128>(p, err, st);
+        return tn == 256 ? launch<E, EPI_LINEAR, false, 256>(p, count, err, st)
+                         : launch<E, EPI_LINEAR, false, 128>(p, count, err, st);
     if (kind == EPI_GATED)
-        return tn == 256 ? launch<E, EPI_GATED, false, 256>(p, err, st) : launch<E, EPI_GATED, false, 128>(p, err, st);
-    return tn == 256 ? launch<E, EPI_GATED_BWD, false, 256>(p, err, st)
-                     : launch<E, EPI_GATED_BWD, false, 128>(p, err, st);
+        return tn == 256 ? launch<E, EPI_GATED, false, 256>(p, count, err, st)
+                         : launch<E, EPI_GATED, false, 128>(p, count, err, st);
+    return tn == 256 ? launch<E, EPI_GATED_BWD, false, 256>(p, count, err, st)
+                     : launch<E, EPI_GATED_BWD, false, 128>(p, count, err, st);
 }
 
 }  // namespace
@@ -436,9 +473,9 @@ PFN_encode encode_fn() {
     return fn;
 }
 
-cudaError_t launch_pairs(const Product& p, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st) {
-    return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, tn, err, st)
-                                : launch_kind<__half>(p, kind, tn, err, st);
+cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st) {
+    return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, count, kind, tn, err, st)
+                                : launch_kind<__half>(p, count, kind, tn, err, st);
 }
 
 }  // namespace dense

@@ -132,25 +132,60 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kb0 = (int)((long long)kall * rank / q.split), nkb = (int)((long long)kall * (rank + 1) / q.split) - kb0;
     const int stage = kP + q.q_bytes;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < q.stages; ++i) {
-            tc::mbar_init(&S.full[i], 1);
-            tc::mbar_init(&S.empty[i], 1);
+    const int pre = min(q.stages, nkb);  // the ring's first round finds it empty
+    auto load_p = [&](int i, int s) {
+        uint8_t* a = ring + s * stage;
+        const int k = (kb0 + i) * BK;
+        if (p.b_mn) {
+            tc::tma_load_2d(a, &tp, &S.full[s], f0, k);
+            tc::tma_load_2d(a + kP / 2, &tp, &S.full[s], f0 + 64, k);
+        } else {
+            tc::tma_load_2d(a, &tp, &S.full[s], k, f0);
+            tc::tma_load_2d(a + kP / 2, &tp, &S.full[s], k, f0 + (KIND == EPI_GATED ? p.e.cols : 64));
         }
-        for (int i = 0; i < 8; ++i) {
-            tc::mbar_init(&S.acc_full[i], 1);
-            tc::mbar_init(&S.acc_empty[i], 4);
+    };
+    auto load_q = [&](int i, int s) {
+        uint8_t* b = ring + s * stage + kP;
+        const int k = (kb0 + i) * BK;
+        if (p.a_mn)
+            for (int c = 0; c * 8192 < q.q_bytes; ++c) tc::tma_load_2d(b + c * 8192, &tq, &S.full[s], t0 + 64 * c, k);
+        else tc::tma_load_2d(b, &tq, &S.full[s], k, t0);
+    };
+    // The producer does not wait for the block: its first loads go out while
+    // TMEM is allocated, and it has no use for the address.
+    if (warp == 0) {
+        const bool lead = tc::elect_one();
+        if (lead) {
+            for (int i = 0; i < q.stages; ++i) {
+                tc::mbar_init(&S.full[i], 1);
+                tc::mbar_init(&S.empty[i], 1);
+            }
+            for (int i = 0; i < 8; ++i) {
+                tc::mbar_init(&S.acc_full[i], 1);
+                tc::mbar_init(&S.acc_empty[i], 4);
+            }
+            tc::mbar_init(&S.drain, 1);
+            tc::fence_barrier_init();
+            tc::tma_prefetch(&tp);
+            tc::tma_prefetch(&tq);
         }
-        tc::mbar_init(&S.drain, 1);
-        tc::fence_barrier_init();
-        tc::tma_prefetch(&tp);
-        tc::tma_prefetch(&tq);
+        __syncwarp();
+        asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
+        if (!q.early) pdl_wait();
+        if (lead)
+            for (int i = 0; i < pre; ++i) {
+                tc::mbar_arrive_expect_tx(&S.full[i], stage);
+                load_p(i, i);
+                if (!q.early) load_q(i, i);
+            }
+        __syncwarp();
+    } else {
+        if (warp == 2) tc::tmem_alloc(&S.tmem, q.cols);
+        tc::fence_before_sync();
+        asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+        tc::fence_after_sync();
     }
-    if (warp == 2) tc::tmem_alloc(&S.tmem, q.cols);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = S.tmem;
+    const uint32_t tmem = warp == 0 ? 0 : *reinterpret_cast<volatile uint32_t*>(&S.tmem);
     if (q.trigger && warp == 3) {  // what ran before this kernel is done before the next one starts
         pdl_wait();
         pdl_trigger();
@@ -160,34 +195,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---- producer
         const bool lead = tc::elect_one();
         bool ok = true;
-        const int rows2 = KIND == EPI_GATED ? p.e.cols : 64;  // the tile's second half of B
-        auto load_p = [&](int i, int s) {
-            uint8_t* a = ring + s * stage;
-            const int k = (kb0 + i) * BK;
-            if (p.b_mn) {
-                tc::tma_load_2d(a, &tp, &S.full[s], f0, k);
-                tc::tma_load_2d(a + kP / 2, &tp, &S.full[s], f0 + 64, k);
-            } else {
-                tc::tma_load_2d(a, &tp, &S.full[s], k, f0);
-                tc::tma_load_2d(a + kP / 2, &tp, &S.full[s], k, f0 + rows2);
-            }
-        };
-        auto load_q = [&](int i, int s) {
-            uint8_t* b = ring + s * stage + kP;
-            const int k = (kb0 + i) * BK;
-            if (p.a_mn)
-                for (int c = 0; c * 8192 < q.q_bytes; ++c) tc::tma_load_2d(b + c * 8192, &tq, &S.full[s], t0 + 64 * c, k);
-            else tc::tma_load_2d(b, &tq, &S.full[s], k, t0);
-        };
-        // the ring's first round finds it empty
-        const int pre = min(q.stages, nkb);
-        if (!q.early) pdl_wait();
-        if (lead)
-            for (int i = 0; i < pre; ++i) {
-                tc::mbar_arrive_expect_tx(&S.full[i], stage);
-                load_p(i, i);
-                if (!q.early) load_q(i, i);
-            }
         if (q.early) {
             pdl_wait();
             if (lead)
@@ -323,8 +330,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_wait();
     __syncwarp();
     __syncthreads();
-    tc::cluster_arrive();
-    tc::cluster_wait();
+    if (q.split > 1) {
+        tc::cluster_arrive();
+        tc::cluster_wait();
+    }
 
     // ---- the tile's sum over the cluster, and the epilogue
     if (q.split == 1) reduce<E, KIND, 1>(p.e, ring, q.nt, rank, t0, f0);
@@ -332,8 +341,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     else if (q.split == 4) reduce<E, KIND, 4>(p.e, ring, q.nt, rank, t0, f0);
     else reduce<E, KIND, 8>(p.e, ring, q.nt, rank, t0, f0);
     // no CTA leaves while another may read its partial
-    tc::cluster_arrive();
-    tc::cluster_wait();
+    if (q.split > 1) {
+        tc::cluster_arrive();
+        tc::cluster_wait();
+    }
     tc::fence_after_sync();
     if (warp == 2) tc::tmem_dealloc(tmem, q.cols);
 }
