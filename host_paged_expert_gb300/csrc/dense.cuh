@@ -62,11 +62,14 @@ struct Product {
     Epi e;
 };
 
-// Place of a product in a chain of launches of one call: CHAIN_BEFORE: the
-// next launch is a product whose B does not depend on this one; CHAIN_AFTER:
-// this product's B does not depend on the launch before it, whose own
-// predecessors are done by the time it lets this one start.
-enum { CHAIN_NONE = 0, CHAIN_BEFORE = 1, CHAIN_AFTER = 2 };
+// Every kernel of the dense operators is launched programmatically: it waits
+// for the launch before it to be done (pdl_wait) before it touches global
+// memory, and does not let the next one start before that (by pdl_trigger, or
+// by its end), so whatever ran two launches back is done by the time a kernel
+// runs.  CHAIN_AFTER: the
+// launch before this product is one of the same call that does not write its
+// B, so B may be read before the wait.
+enum { CHAIN_NONE = 0, CHAIN_AFTER = 1 };
 
 // elem: pe_elem of the 16-bit operands and of every 16-bit tensor of the epilogue.
 cudaError_t launch_product(const Product& p, EpiKind kind, int elem, int chain, uint32_t* err, cudaStream_t st);

@@ -273,7 +273,7 @@ extern "C" pe_status pe_gated_ffn(const void* x, int64_t x_stride, const void* w
         p.e.ld_out = intermediate;
         p.e.keep = keep;
         p.e.ld_keep = 2 * (int64_t)intermediate;
-        e = launch_product(p, EPI_GATED, elem, CHAIN_BEFORE, err, st);
+        e = launch_product(p, EPI_GATED, elem, CHAIN_NONE, err, st);
     }
     if (!e) {
         Product p = make(workspace, intermediate, 0, w2, intermediate, 0, rows, hidden, intermediate);

@@ -186,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
     pdl_wait();
+    if (warp == 3) pdl_trigger();
 
     if (warp < 4) {
         if (FP8) tc::reg_dec<kRegsFew>();

@@ -20,11 +20,14 @@ namespace dense {
 namespace {
 
 constexpr int kWarps = 8, kAhead = 4;
+// Blocks up to which the next launch may move in early: beyond, its waiting
+// blocks take the room of this one's last ones (1 x 8192 x 8192: 21.5 us
+// instead of 18.8).
+constexpr unsigned kLetGo = 1216;
 
 struct Plan {
     int share;    // warps per pair of rows
     int early;    // ask for weights before the previous kernel is done
-    int trigger;  // let the next kernel start early
 };
 
 template <typename E>
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(const __grid_constant
     if (!q.early) pdl_wait();
     fetch(c);
     if (q.early) pdl_wait();
-    if (q.trigger) pdl_trigger();
+    if (gridDim.x <= kLetGo) pdl_trigger();
     while (c - lane < pieces) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -152,8 +155,7 @@ template <typename E, int KIND, bool FP8>
 cudaError_t launch(const Product& p, int chain, cudaStream_t st) {
     constexpr int PER = KIND == EPI_GATED ? 1 : 2;  // result columns of a group
     Plan q = {};
-    q.early = chain & CHAIN_AFTER ? 1 : 0;
-    q.trigger = chain & CHAIN_BEFORE ? 1 : 0;
+    q.early = chain == CHAIN_AFTER;
     const int pieces = p.K / (FP8 ? 16 : 8);
     auto blocks = [&](int share) { return (int)(((long long)p.e.cols + PER * (kWarps / share) - 1) / (PER * (kWarps / share))); };
     // warps share rows until there are two blocks per SM, as long as each lane

@@ -48,7 +48,6 @@ struct Plan {
     int sub_len;  // stages that one of them takes (16-bit operands)
     int cols;     // TMEM columns
     int early;    // load weights before the previous kernel is done
-    int trigger;  // let the next kernel start early
 };
 
 struct Shared {
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc::fence_after_sync();
     }
     const uint32_t tmem = warp == 0 ? 0 : *reinterpret_cast<volatile uint32_t*>(&S.tmem);
-    if (q.trigger && warp == 3) {  // what ran before this kernel is done before the next one starts
+    if (warp == 3) {  // what ran before this kernel is done before the next one starts
         pdl_wait();
         pdl_trigger();
     }
@@ -411,8 +410,7 @@ cudaError_t launch(const Product& p, const SplitShape& s, int chain, uint32_t* e
     q.ftiles = (p.e.cols + NF - 1) / NF;
     const long long blocks = (long long)q.ftiles * ((p.M + s.nt - 1) / s.nt) * s.split;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    q.early = chain & CHAIN_AFTER ? 1 : 0;
-    q.trigger = chain & CHAIN_BEFORE ? 1 : 0;
+    q.early = chain == CHAIN_AFTER;
     CUtensorMap tp, tq;
     if (!encode(&tp, p.b, p.ldb, p.N, p.K, p.b_mn, FP8, 64) || !encode(&tq, p.a, p.lda, p.M, p.K, p.a_mn, FP8, s.nt))
         return cudaErrorInvalidValue;
