@@ -2,7 +2,7 @@
 
 Every .cu file under csrc/ is compiled in parallel to an object file, then
 linked into ``host_paged_expert_gb300/libpe.so``; the Python binding of the
-dense operators (csrc/py_dense.c) becomes ``_dense.so`` next to it.  Run as
+dense operators (csrc/py_dense.cpp) becomes ``_dense.so`` next to it.  Run as
 ``python -m host_paged_expert_gb300.build`` or call ``build()``.
 """
 
@@ -52,29 +52,51 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     extra = list(extra or [])
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)  # the longest one first
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_binding()
+    _link_binding(binding)
     return LIB
 
 
-def _build_binding() -> None:
-    """Compile the CPython binding and link it against libpe.so beside it."""
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if not cc:
-        raise RuntimeError("no C compiler found")
-    tmp = PYEXT + ".tmp"
-    cmd = [cc, "-O2", "-shared", "-fPIC", "-Wall", "-Werror", f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(ROOT, 'include')}",
-           os.path.join(CSRC, "py_dense.c"), f"-L{PKG}", "-l:libpe.so", "-Wl,-rpath,$ORIGIN", "-o", tmp]
+def _compile_binding() -> str:
+    """Compile the CPython binding of the dense operators."""
+    import torch
+
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found")
+    tinc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    obj = os.path.join(BUILD, "py_dense.o")
+    cmd = [cxx, "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-sign-compare",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{os.path.join(ROOT, 'include')}", f"-isystem{tinc}", f"-isystem{os.path.join(tinc, 'torch', 'csrc', 'api', 'include')}",
+           f"-isystem{cuda}", "-c", os.path.join(CSRC, "py_dense.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"building the binding failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"compiling the binding failed:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Link it against libpe.so beside it and torch's libraries."""
+    import torch
+
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = PYEXT + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-shared", obj, f"-L{PKG}", "-l:libpe.so", f"-L{tlib}", "-ltorch_python", "-ltorch_cuda",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PYEXT)
 
 

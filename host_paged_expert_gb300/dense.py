@@ -57,7 +57,7 @@ _native = None
 
 
 def _c():
-    """The binding (csrc/py_dense.c), built in-tree next to libpe.so."""
+    """The binding (csrc/py_dense.cpp), built in-tree next to libpe.so."""
     global _native
     if _native is None:
         lib()  # raises if libpe is not built
@@ -66,8 +66,7 @@ def _c():
         except ImportError as e:
             raise RuntimeError(f"_dense.so is not built ({os.path.dirname(__file__)}); "
                                "run host_paged_expert_gb300.build.build()") from e
-        m.setup(torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.bfloat16, torch.float16,
-                torch.float32, torch.float8_e4m3fn, torch.uint8, _ACT, _raise, _elsewhere, RmsNorm)
+        m.setup(_ACT, _raise, _elsewhere, RmsNorm)
         _native = m
     return _native
 

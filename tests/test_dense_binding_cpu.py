@@ -1,8 +1,8 @@
-"""The native binding of the dense operators without a GPU: stand-ins for
-torch's tensors and allocator go through its checks, its results and its
-refusals (calls with no rows return before they touch a device)."""
+"""The native binding of the dense operators without a GPU: it says what is
+wrong with an argument before it asks where the tensors are, so CPU tensors
+bring out each of its refusals, and a call with nothing wrong is refused for
+its device alone."""
 
-import importlib
 import os
 
 import pytest
@@ -10,92 +10,84 @@ import torch
 
 from host_paged_expert_gb300 import _lib, dense
 
-BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+BF, HF, F32, F8 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
 
 
-class Fake:
-    """What the binding reads of a tensor."""
-
-    def __init__(self, shape, dtype, dev=0, stride=None):
-        self.shape, self.dtype, self.device, self._dev = tuple(shape), dtype, "cuda:0", dev
-        row = [1]
-        for d in reversed(shape[1:]):
-            row.insert(0, row[0] * d)
-        self._stride = tuple(stride or row)
-
-    def stride(self):
-        return self._stride
-
-    def get_device(self):
-        return self._dev
-
-    def data_ptr(self):
-        return 1 << 20
-
-
-@pytest.fixture
-def m():
+@pytest.fixture(scope="module", autouse=True)
+def built():
     if not (os.path.exists(_lib.LIB_PATH) and os.path.exists(os.path.join(os.path.dirname(_lib.LIB_PATH), "_dense.so"))):
         from host_paged_expert_gb300 import build
 
         build.build()
-    _lib.lib()
-    mod = importlib.import_module("host_paged_expert_gb300._dense")
-    mod.setup(lambda *shape, dtype, device: Fake(shape, dtype), lambda dev: 0, lambda: 0, BF, torch.float16, F32, F8, torch.uint8,
-              dense._ACT, dense._raise, dense._elsewhere, dense.RmsNorm)
-    yield mod
-    dense._native = None  # the next real call sets the binding up again
 
 
-X, W = Fake((0, 64), BF), Fake((64,), BF)
+def t(*shape, dt=BF):
+    return torch.zeros(*shape, dtype=dt)
 
 
-def test_results(m):
-    r = m.rms_norm(X, W, None, 1e-6, True, True, True, None)
-    assert r.sum is X and r.y.shape == (0, 64) and r.codes.dtype == F8 and r.scale.shape == (0, 1) and r.rstd.shape == (0,)
-    r = m.rms_norm(X, W, X, 1e-6, False, False, False, None)
-    assert r.sum is not X and r.sum.shape == (0, 64) and r.y is None and r.codes is None and r.rstd is None
-    w, b = Fake((24, 64), BF), Fake((24,), BF)
-    y, z = m.linear(X, w, b, "silu", Fake((0, 24), BF), None, None, None, True, None)
-    assert y.shape == z.shape == (0, 24) and y.dtype == BF
-    y, z = m.linear(X, w, None, "none", None, None, None, F32, True, None)
-    assert z is None and y.dtype == F32
-    sc = (Fake((0, 1), F32), Fake((1, 1), F32))
-    assert m.linear(Fake((0, 64), F8), Fake((24, 64), F8), None, "none", None, *sc, None, False, None).dtype == BF
-    assert m.linear(Fake((0, 64), F8), Fake((24, 64), F8), None, "none", Fake((0, 24), torch.float16), *sc, None, False,
-                    None).dtype == torch.float16
-    w13, w2 = Fake((32, 64), BF), Fake((64, 16), BF)
-    y, gu = m.gated_ffn(X, w13, w2, "silu", None, True, None)
-    assert y.shape == (0, 64) and gu.shape == (0, 32)
-    assert m.gated_ffn(X, w13, w2, "silu", X, False, None).shape == (0, 64)
+X, X0, N, W, W13, W2 = t(4, 64), t(0, 64), t(64), t(24, 64), t(32, 64), t(64, 16)
+SC = dict(x_scale=t(4, 1, dt=F32), w_scale=t(1, 1, dt=F32))
 
 
-def test_refusals(m):
-    x4, w = Fake((4, 64), BF), Fake((24, 64), BF)
-    w13, w2 = Fake((32, 64), BF), Fake((64, 16), BF)
-    none = (None, "none", None, None, None, None, False, None)
-    for call in (
-        lambda: m.rms_norm(X, Fake((32,), BF), None, 1e-6, True, False, False, None),
-        lambda: m.rms_norm(X, W, Fake((1, 64), BF), 1e-6, True, False, False, None),
-        lambda: m.rms_norm(Fake((4, 64), BF, stride=(1, 4)), W, None, 1e-6, True, False, False, None),
-        lambda: m.rms_norm(Fake((4, 64), F32), Fake((64,), F32), None, 1e-6, True, False, False, None),
-        lambda: m.linear(X, w, None, "tanh", None, None, None, None, False, None),
-        lambda: m.linear(X, W, *none),
-        lambda: m.linear(x4, Fake((24, 64), BF, stride=(1, 24)), *none),
-        lambda: m.linear(Fake((4, 60), BF), Fake((24, 60), BF), *none),
-        lambda: m.linear(Fake((4, 64), BF, dev=-1), w, *none),
-        lambda: m.linear(x4, Fake((24, 64), BF, dev=1), *none),
-        lambda: m.linear(Fake((4, 64), F8), Fake((24, 64), F8), *none),
-        lambda: m.linear(Fake((1 << 31, 64), BF), w, *none),
-        lambda: m.linear_backward(Fake((4, 24), BF), x4, w, None, "silu", False, None),
-        lambda: m.gated_ffn(X, Fake((31, 64), BF), w2, "silu", None, False, None),
-        lambda: m.gated_ffn(X, w13, W, "silu", None, False, None),
-        lambda: m.gated_ffn_backward(x4, x4, w13, w2, Fake((4, 16), BF), "silu", None),
-        lambda: m.rms_norm_backward(x4, x4, W, Fake((3,), F32), None, None),
-    ):
-        with pytest.raises(_lib.PEError):
-            call()
-    with pytest.raises(AttributeError):
-        m.linear(1, 2, *none)
+@pytest.mark.parametrize("call,says", [
+    (lambda: dense.rms_norm(t(4, 64, dt=F32), t(64, dt=F32)), "neither bf16 nor fp16"),
+    (lambda: dense.rms_norm(t(2, 2, 64), N), "want a matrix"),
+    (lambda: dense.rms_norm(t(64, 4).t(), N), "columns must be contiguous"),
+    (lambda: dense.rms_norm(X, N[:32]), "weight: want contiguous BFloat16 [64]"),
+    (lambda: dense.rms_norm(X, N.half()), "weight: want contiguous BFloat16 [64], got Half"),
+    (lambda: dense.rms_norm(X, t(128)[::2]), "weight: want contiguous"),
+    (lambda: dense.rms_norm(X, N, X[:3]), "residual: want BFloat16 [4, 64]"),
+    (lambda: dense.rms_norm_backward(X, X, N, t(3, dt=F32)), "rstd: want contiguous Float [4]"),
+    (lambda: dense.rms_norm_backward(X[:, :32], X, N, t(4, dt=F32)), "dy: want"),
+    (lambda: dense.rms_norm_backward(X, X, N, t(4, dt=F32), X[1:]), "dsum: want"),
+    (lambda: dense.linear(X, W.t()), "weight: want"),
+    (lambda: dense.linear(X, N), "weight: want"),
+    (lambda: dense.linear(X, t(64, 24).t()), "weight: want"),
+    (lambda: dense.linear(X, W.half()), "weight: want"),
+    (lambda: dense.linear(X, W, act="tanh"), "unknown activation 'tanh'"),
+    (lambda: dense.linear(X, W, bias=N), "bias: want contiguous BFloat16 [24]"),
+    (lambda: dense.linear(X, W, residual=X), "residual: want BFloat16 [4, 24]"),
+    (lambda: dense.linear(X, W, out_dtype=HF), "out_dtype"),
+    (lambda: dense.linear(X, W, **SC), "scales go with E4M3"),
+    (lambda: dense.linear(X.to(F8), W.to(F8)), "need x_scale and w_scale"),
+    (lambda: dense.linear(X.to(F8), W.to(F8), x_scale=t(4, 2, dt=F32), w_scale=SC["w_scale"]), "x_scale: want"),
+    (lambda: dense.linear(X.to(F8), W.to(F8), residual=t(4, 24, dt=F32), **SC), "neither bf16 nor fp16"),
+    (lambda: dense.linear(t(1, 8).expand(1 << 32, 8), t(4, 8)), "too large"),
+    (lambda: dense.linear_backward(t(4, 24), X, W, act="silu"), "needs the z"),
+    (lambda: dense.linear_backward(t(4, 24), X, W, t(4, 23), "silu"), "z: want"),
+    (lambda: dense.linear_backward(t(4, 23), X, W), "dy: want"),
+    (lambda: dense.gated_ffn(X, t(31, 64), W2), "w13: want contiguous BFloat16 [32, 64]"),
+    (lambda: dense.gated_ffn(X, W13, W2[:, :8]), "w13: want contiguous BFloat16 [16, 64]"),
+    (lambda: dense.gated_ffn(X, W13, N), "w13: want"),
+    (lambda: dense.gated_ffn(X, W13, t(16, 64).t()), "w2: want"),
+    (lambda: dense.gated_ffn_backward(X, X, W13, W2, t(4, 16)), "gu: want"),
+    # nothing else is wrong with these
+    (lambda: dense.rms_norm(X, N, X, quant=True, save=True), "want CUDA tensors"),
+    (lambda: dense.rms_norm(t(4, 128)[:, :64], N), "want CUDA tensors"),
+    (lambda: dense.rms_norm_backward(X, X, N, t(4, dt=F32), X), "want CUDA tensors"),
+    (lambda: dense.linear(X, W, t(24), "silu", t(4, 24), out_dtype=F32, save=True), "want CUDA tensors"),
+    (lambda: dense.linear(X.to(F8), W.to(F8), t(24, dt=HF), **SC), "want CUDA tensors"),
+    (lambda: dense.linear(X0, W), "want CUDA tensors"),
+    (lambda: dense.linear_backward(t(4, 24), X, W, t(4, 24), "silu", bias=True), "want CUDA tensors"),
+    (lambda: dense.gated_ffn(X, W13, W2, "gelu", X, save=True), "want CUDA tensors"),
+    (lambda: dense.gated_ffn_backward(X, X, W13, W2, t(4, 32)), "want CUDA tensors"),
+])
+def test_refuses(call, says):
+    with pytest.raises(_lib.PEError) as e:
+        call()
+    assert says in str(e.value)
+    assert e.value.status in (_lib.PE_ERR_INVALID, _lib.PE_ERR_RANGE)
+
+
+def test_refuses_what_is_no_tensor():
     with pytest.raises(TypeError):
-        m.linear(1, 2)
+        dense.linear(1, 2)
+    with pytest.raises(TypeError):
+        dense.rms_norm(X, [1.0] * 64)
+    with pytest.raises(TypeError):
+        dense.linear(X, W, out_dtype="float32")
+    with pytest.raises(TypeError):
+        dense.rms_norm(X, N, eps="small")
+    for _ in range(2000):  # the error paths hold on to nothing
+        with pytest.raises(_lib.PEError):
+            dense.linear(X, W, bias=N)
