@@ -204,10 +204,21 @@ __device__ __forceinline__ void store8_f32(float* p, bool vec, int n, const floa
     }
 }
 
-// tanh(x) = 1 - 2 / (1 + e^2x): about 1e-7 absolute, enough for results that
-// are rounded to 16 bits; saturates to +-1.
-__device__ __forceinline__ float tanh_f(float x) { return 1.f - __fdividef(2.f, 1.f + __expf(2.f * x)); }
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// e^x and 1/y to about 2 ulp by the special-function unit, subnormals as
+// zero: results are rounded to 16 bits, and y is at least 1 here.
+__device__ __forceinline__ float exp_f(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ float rcp_f(float y) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    return r;
+}
+// tanh(x) = 1 - 2 / (1 + e^2x): about 1e-7 absolute; saturates to +-1.
+__device__ __forceinline__ float tanh_f(float x) { return fmaf(-2.f, rcp_f(1.f + exp_f(2.f * x)), 1.f); }
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp_f(1.f + exp_f(-x)); }
 
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 constexpr float kGeluCubic = 0.044715f;
@@ -232,7 +243,7 @@ __device__ __forceinline__ float act_both(int act, float z, float& d) {
         }
         case PE_ACT_GELU: {
             const float c = 0.5f + 0.5f * erff(z * 0.70710678118654752f);
-            d = c + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
+            d = c + z * exp_f(-0.5f * z * z) * 0.3989422804014327f;
             return z * c;
         }
         case PE_ACT_GELU_TANH: {
@@ -278,10 +289,10 @@ struct EpiIn {
     int4 a, b;
 };
 
-// Whether the epilogue is at most a bias and a residual, in vectors.
+// Whether the epilogue keeps nothing and stores 16-bit vectors.
 template <int KIND>
 __device__ __forceinline__ bool epi_light(const Epi& e) {
-    return KIND == EPI_LINEAR && e.vec && !e.keep && !e.out_f32 && e.act == PE_ACT_NONE;
+    return KIND == EPI_LINEAR && e.vec && !e.keep && !e.out_f32;
 }
 
 // bias of columns col..col+7
@@ -355,6 +366,25 @@ __device__ __forceinline__ void epi_store(const Epi& e, int row, int col, const 
         store8(o + e.cols, true, 8, a);
         if (e.h) store8(static_cast<E*>(e.h) + row * (int64_t)e.cols + col, true, 8, w);
     }
+}
+
+// epi_store where epi_light holds, with a third less code.
+template <typename E, int ACT>
+__device__ __forceinline__ void epi_store_light(const Epi& e, int row, int col, const float (&bias)[8], const EpiIn& in,
+                                                float (&v)[8]) {
+    if (e.bias)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += bias[i];
+    if (ACT != PE_ACT_NONE)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_fwd(ACT, v[i]);
+    if (e.res) {
+        float r[8];
+        unpack8<E>(in.a, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+    if (row < e.rows && col < e.cols) store8(static_cast<E*>(e.out) + row * e.ld_out + col, true, 8, v);
 }
 
 // The same for a single element (EPI_LINEAR, EPI_GATED).

@@ -88,33 +88,23 @@ template <typename E, int KIND>
 __device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, int lane, int row0, int col0,
                                           const Ahead<E, KIND>& x) {
     const int c8 = lane & 3, row = row0 + (lane >> 2), col = col0 + 8 * c8;
-    if (epi_light<KIND>(e)) {
-        E* out = static_cast<E*>(e.out) + row * e.ld_out + col;
-        if (col < e.cols)
+    with_act(e.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (epi_light<KIND>(e)) {
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 float v[8];
                 patch_get(patch, it * 8 + (lane >> 2), c8, v);
-                if (e.bias)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += x.bias[i];
-                if (e.res) {
-                    float r[8];
-                    unpack8<E>(x.in[it].a, r);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += r[i];
-                }
-                if (row + it * 8 < e.rows) store8(out + it * 8 * e.ld_out, true, 8, v);
+                epi_store_light<E, ACT>(e, row + it * 8, col, x.bias, x.in[it], v);
             }
-        return;
-    }
-    with_act(e.act, [&](auto act) {
+        } else {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            float v[8], u[8];
-            patch_get(patch, it * 8 + (lane >> 2), c8, v);
-            if (KIND == EPI_GATED) patch_get(patch + 4096, it * 8 + (lane >> 2), c8, u);
-            epi_store<E, KIND, decltype(act)::value>(e, row + it * 8, col, x.bias, x.in[it], v, u);
+            for (int it = 0; it < 4; ++it) {
+                float v[8], u[8];
+                patch_get(patch, it * 8 + (lane >> 2), c8, v);
+                if (KIND == EPI_GATED) patch_get(patch + 4096, it * 8 + (lane >> 2), c8, u);
+                epi_store<E, KIND, ACT>(e, row + it * 8, col, x.bias, x.in[it], v, u);
+            }
         }
     });
 }

@@ -20,10 +20,11 @@ namespace dense {
 namespace {
 
 constexpr int kWarps = 8, kAhead = 4;
-// Blocks up to which the next launch may move in early: beyond, its waiting
-// blocks take the room of this one's last ones (1 x 8192 x 8192: 21.5 us
-// instead of 18.8).
-constexpr unsigned kLetGo = 1216;
+// Weight bytes up to which the next launch may move in early: it hides the
+// next one's start (1 x 4096 x 2048, 17 MB: 2.9 instead of 3.0 us), but its
+// waiting blocks slow a long stream (1 x 8192 x 8192, 134 MB: 21.5 us instead
+// of 18.8).
+constexpr size_t kLetGo = 32u << 20;
 
 struct Plan {
     int share;    // warps per pair of rows
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(const __grid_constant
     if (!q.early) pdl_wait();
     fetch(c);
     if (q.early) pdl_wait();
-    if (gridDim.x <= kLetGo) pdl_trigger();
+    if ((size_t)p.N * p.K * ES <= kLetGo) pdl_trigger();
     while (c - lane < pieces) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {

@@ -107,8 +107,12 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int u = ub + i * kThreads;
-                if (u < total)
-                    epi_store<E, KIND, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0], v[i][G - 1]);
+                if (u < total) {
+                    if (epi_light<KIND>(e))
+                        epi_store_light<E, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0]);
+                    else
+                        epi_store<E, KIND, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0], v[i][G - 1]);
+                }
             }
         });
     }
