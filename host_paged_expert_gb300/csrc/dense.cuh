@@ -93,6 +93,8 @@ constexpr int kGemvRows = 4;
 cudaError_t launch_gemv(const Product& p, EpiKind kind, int elem, int chain, cudaStream_t st);
 // K blocks of 64 that one accumulator takes where the result is fp32, of kb in all.
 int split_blocks(const SplitShape& s, int kb);
+// CTAs of this shape that the current device holds at once.
+int split_resident(const SplitShape& s);
 
 using PFN_encode = PFN_cuTensorMapEncodeTiled_v12000;
 

@@ -1,23 +1,24 @@
 // Which kernel and which tiles a matrix product takes: the least of the
 // times that these models give.  They were fitted to GB300 measurements of
-// both kernels (plain bf16 products, operands in L2, in microseconds) and
-// agree with them to about 10 % from one row to 2048:
+// both kernels (70 plain bf16 products of 8 to 2048 rows, operands in L2, in
+// microseconds), agree with them to 8 % and choose a shape 1 % slower than
+// the best one on average:
 //
 //   rows x K x cols   CTA pairs, 256 / 128 columns   cluster split (tokens, CTAs along K)
-//   1 x 2048 x 2048        13.9 / -                  11.5 (16, 1)   7.8 (16, 2)   5.5 (16, 8)
-//   64 x 4096 x 4096       25.4 / -                  21.2 (64, 1)  13.7 (64, 2)  10.5 (64, 4)
-//   256 x 2048 x 2048      17.1 / 12.7               13.4 (64, 1)  10.0 (64, 2)  11.3 (64, 4)
-//   512 x 8192 x 1024      42.3 / 31.4               37.0 (64, 1)  21.9 (64, 2)  17.9 (128, 4)
-//   1024 x 2048 x 2048     17.1 / 13.1               17.1 (64, 1)  21.9 (64, 2)  16.3 (128, 1)
-//   1024 x 4096 x 4096     26.6 / 32.8               49.3 (64, 1)
+//   8 x 2048 x 2048        13.3 / 9.8                 9.8 (16, 1)   6.8 (16, 2)   5.0 (16, 4)   4.5 (16, 8)
+//   64 x 4096 x 4096       22.1 / 16.5               18.8 (64, 1)  12.4 (64, 2)   9.5 (64, 4)  11.9 (64, 8)
+//   256 x 2048 x 2048      14.1 / 10.5               11.1 (64, 1)   8.7 (64, 2)  10.2 (64, 4)  20.4 (64, 8)
+//   400 x 8192 x 1024      39.4 / 29.5               34.8 (64, 1)  20.7 (64, 2)  17.8 (64, 4)  15.9 (128, 4)
+//   1024 x 2048 x 2048     14.2 / 11.1               14.1 (64, 1)  21.2 (64, 2)  37.0 (64, 4)  13.2 (128, 1)
+//   2048 x 4096 x 4096     41.0 / 57.4               87.5 (64, 1)
 //
 //   rows x K x cols   warps streaming weights        best cluster split
-//   1 x 4096 x 2048         2.7                       6.8
-//   1 x 8192 x 8192        18.6                      24.2
-//   2 x 4096 x 4096         6.2                       8.2
-//   4 x 2048 x 2048         4.0                       5.7
-//   4 x 8192 x 8192        40.4                      24.4
-//   8 x 2048 x 2048         8.1                       6.1
+//   1 x 4096 x 2048         2.7                       5.2
+//   1 x 8192 x 8192        19.8                      23.1
+//   2 x 4096 x 4096         6.0                       6.7
+//   4 x 2048 x 2048         3.9                       4.3
+//   4 x 4096 x 4096         9.7                       6.5
+//   4 x 8192 x 8192        40.4                      23.2
 #include <algorithm>
 #include <cmath>
 
@@ -31,32 +32,37 @@ constexpr double kSms = 152, kPairs = 76;
 
 int up(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// Launch, filling the pipeline and the last tile's epilogue; then the K
-// blocks of each wave of tiles, under which the other epilogues hide unless K
-// is short.  8-bit operands: every tile's epilogue is exposed (its warps add
-// up the K blocks), 3.3 us.
+// Of a launch of CTA pairs: starting it, filling the pipeline and the last
+// tile's epilogue (`full` of it for tiles with all their rows); a K block of
+// a tile; and what of a tile's epilogue shows if its K blocks are short.
+struct PairCost {
+    double fixed, full, block, epi;
+};
+constexpr PairCost kWide = {4.8, 1.1, 0.264, 1.75}, kNarrow = {3.4, 0.45, 0.219, 0.93};  // 256, 128 columns
+
+// 8-bit operands: every tile's epilogue is exposed (its warps add up the K
+// blocks), 3.3 us.
 double pair_time(const Product& p, EpiKind kind, int tn) {
     const bool fp8 = p.a_scale != nullptr;
     const int kb = up(p.K, fp8 ? 128 : 64), cols = kind == EPI_GATED ? tn / 2 : tn;
     const double waves = std::max(1.0, std::ceil((double)up(p.M, 256) * up(p.e.cols, cols) / kPairs));
-    if (fp8) return 5.5 + waves * (kb * 0.46 + 3.3);
-    const double block = tn == 256 ? 0.265 : 0.195, epi = tn == 256 ? 3.5 : 1.8;
-    const double full = tn == 256 ? 3.1 : 1.6, fixed = tn == 256 ? 5.5 : 4.7;
-    return fixed + full * std::min(1.0, p.M / 256.0) + waves * kb * block + (waves - 1) * std::max(0.0, epi - kb * block);
+    if (fp8) return 3.0 + waves * (kb * 0.45 + 3.3);
+    const PairCost& c = tn == 256 ? kWide : kNarrow;
+    return c.fixed + c.full * std::min(1.0, p.M / 256.0) + waves * kb * c.block + (waves - 1) * std::max(0.0, c.epi - kb * c.block);
 }
 
-// The same with the K blocks of one CTA (or all weights from HBM); blocks on one SM share its tensor
-// core; partial sums cross the cluster at about 1.6 TB/s.
+// The same with the K blocks of one CTA, or all weights from HBM; blocks on
+// one SM share its tensor core; partial sums cross the cluster.
 double split_time(const Product& p, EpiKind kind, const SplitShape& s) {
     const bool fp8 = p.a_scale != nullptr;
     const int kb = up(p.K, fp8 ? 128 : 64), share = up(kb, s.split);
     const double base = (double)up(p.e.cols, kind == EPI_GATED ? 64 : 128) * up(p.M, s.nt), ctas = base * s.split;
-    const double block = fp8 ? 0.26 + 0.0045 * s.nt : s.nt <= 64 ? 0.245 : 0.275;
-    const double slots = s.nt <= 64 ? 2 * kSms : kSms;
-    const double fixed = 3.6 + 0.0245 * s.nt, waves = std::max(1.0, std::ceil(ctas / slots));
+    const double block = fp8 ? 0.27 + 0.0033 * s.nt : s.nt <= 64 ? 0.225 : 0.247;
+    const double slots = split_resident(s);  // fewer than the SMs hold: a cluster stays within a GPC
+    const double fixed = 2.05 + 0.0193 * s.nt, waves = std::max(1.0, std::ceil(ctas / slots));
     const double stream = (double)p.N * p.K * (fp8 ? 1 : 2) / 6.2e6;  // the weights at HBM's rate
-    return fixed * waves + std::max(stream, share * block * std::max(1.0, ctas / kSms)) +
-           base * s.nt * 512.0 * (s.split - 1) / 1.6e6 + 0.1 * (s.split - 1);
+    return (fixed + (s.split > 1 ? 0.55 : 0.0)) * waves + std::max(stream, share * block * std::max(1.0, 1.06 * ctas / kSms)) +
+           base * s.nt * 512.0 * (s.split - 1) / 2.1e6 + 0.05 * (s.split - 1);
 }
 
 // Weights at what HBM and L2 gave, or the multiply-adds with operands from L1.
@@ -122,7 +128,8 @@ double group_time(const Product* p, int count, int tn) {
         t += n;
     }
     const double most = *std::max_element(load, load + (int)kPairs);
-    return (tn == 256 ? 8.6 : 6.3) + most * (tn == 256 ? 0.265 : 0.195);
+    const PairCost& c = tn == 256 ? kWide : kNarrow;
+    return c.fixed + c.full + most * c.block;
 }
 
 }  // namespace

@@ -371,7 +371,7 @@ constexpr int kMaxSmem = 226 * 1024;  // what a block may have, less the static 
 // above, one.  Their shared memory (between kTwo and kHalf, or at least kOne
 // bytes) decides how many fit, and their TMEM has to fit as well: a block that
 // waited for columns held by a block of its own cluster would wait forever.
-constexpr int kPairTokens = 64, kTwo = 80 * 1024, kHalf = 112 * 1024, kOne = 116 * 1024;
+constexpr int kPairTokens = 64, kTwo = 80 * 1024, kHalf = 110 * 1024, kOne = 116 * 1024;
 int block_bytes(int nt) { return nt <= kPairTokens ? kHalf : kMaxSmem; }
 int tmem_cols(int nt) { return nt <= kPairTokens ? 256 : 512; }
 
@@ -446,6 +446,34 @@ cudaError_t launch_kind(const Product& p, EpiKind kind, const SplitShape& s, int
 int split_blocks(const SplitShape& s, int kb) {
     const int share = (kb + s.split - 1) / s.split, n = sub_count(s, kb);
     return (share + n - 1) / n;
+}
+
+int split_resident(const SplitShape& s) {
+    static std::atomic<int> known[2][4];  // one or two blocks per SM; 1, 2, 4 or 8 CTAs along K
+    const int two = s.nt <= kPairTokens, at = s.split >= 8 ? 3 : s.split >= 4 ? 2 : s.split - 1;
+    int n = known[two][at].load();
+    if (n) return n;
+    n = 152;  // where the runtime does not say
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)s.split, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)s.split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = block_bytes(s.nt);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto k = split_kernel<__nv_bfloat16, EPI_LINEAR, false>;
+    int c = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&c, k, &cfg) == cudaSuccess && c > 0)
+        n = c * s.split;
+    // The runtime counts one block per SM for a kernel that allocates TMEM;
+    // two do run where they fit (64 x 512 x 19456, 152 blocks: 5.2 us; 304
+    // blocks: 6.5; 305: 10.5).
+    n <<= two;
+    known[two][at].store(n);
+    return n;
 }
 
 cudaError_t launch_split(const Product& p, EpiKind kind, int elem, const SplitShape& s, int chain, uint32_t* err,
