@@ -84,8 +84,8 @@ Choice choose(const Product& p, EpiKind kind) {
     const bool fp8 = p.a_scale != nullptr, f32 = p.e.out_f32 != 0;
     const int kb = up(p.K, fp8 ? 128 : 64);
     Choice c;
-    // fp32 results stay with the kernel that bounds the terms of one accumulator
-    if (!f32 || fp8)
+    // fp32 results of more than 8 blocks stay with the kernel that bounds the terms of one accumulator
+    if (!f32 || fp8 || kb <= 8)
         for (int t = 256; t >= (fp8 ? 256 : 128); t /= 2) {
             const double us = pair_time(p, kind, t);
             if (us < c.us) c.us = us, c.tn = t;

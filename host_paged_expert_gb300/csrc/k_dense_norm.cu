@@ -146,52 +146,57 @@ __global__ void __launch_bounds__(kMostThreads, NV <= 2 ? 2 : 1) rms_norm_kernel
     }
 }
 
-// Block b takes rows b, b + gridDim, ...: dx of each, and the block's share
-// of the weight's gradient in registers, written once to partial[b].  The
-// next row's loads are in flight while a row is reduced.
+// Short rows share a block: its `groups` groups of threads take a row each.
+// Every group keeps its share of the weight's gradient in registers, the
+// groups' shares are added in order through shared memory and written once
+// to partial[block].  The next row's loads are in flight while a row is
+// reduced (NV <= 2, where there are registers for it).
 template <typename E, int NV>
-__global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a, int groups) {
+    constexpr bool AHEAD = NV <= 2;
     __shared__ float red[2][32];
+    __shared__ float share[NV == 1 ? 8 * kMostThreads / 2 : 1];
     pdl_wait();
-    const int vecs = a.hidden >> 3;
-    constexpr bool AHEAD = NV <= 2;  // the next row's loads in flight while there are registers for them
+    const int vecs = a.hidden >> 3, th = blockDim.x / groups, group = threadIdx.x / th, tid = threadIdx.x - group * th;
+    const int w0 = group * (th >> 5), warps = th >> 5;  // the group's first warp, and how many
     float dw[NV][8] = {};
-    int4 sn[NV], yn[NV], dn[NV], w[AHEAD ? NV : 1];
+    int4 sn[NV], yn[NV], dn[NV];
     float rn = 0.f;
-    auto weight = [&](int i) {
-        const int c = i * blockDim.x + threadIdx.x;
-        return c < vecs ? *reinterpret_cast<const int4*>(static_cast<const E*>(a.w) + 8 * c) : make_int4(0, 0, 0, 0);
-    };
     auto fetch = [&](int row) {
         rn = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
+            const int c = i * th + tid;
+            sn[i] = yn[i] = dn[i] = make_int4(0, 0, 0, 0);
             if (c < vecs) {
                 sn[i] = ld_stream(static_cast<const E*>(a.sum) + row * a.ld_sum + 8 * c);
                 yn[i] = ld_stream(static_cast<const E*>(a.dy) + row * a.ld_dy + 8 * c);
-                if (a.dsum && AHEAD) dn[i] = ld_stream(static_cast<const E*>(a.dsum) + row * a.ld_dsum + 8 * c);
+                if (a.dsum) dn[i] = ld_stream(static_cast<const E*>(a.dsum) + row * a.ld_dsum + 8 * c);
             }
         }
     };
+    auto weight = [&](int i) {
+        const int c = i * th + tid;
+        return c < vecs ? *reinterpret_cast<const int4*>(static_cast<const E*>(a.w) + 8 * c) : make_int4(0, 0, 0, 0);
+    };
+    int4 w[AHEAD ? NV : 1];
+    if (AHEAD)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        sn[i] = yn[i] = dn[i] = make_int4(0, 0, 0, 0);
-        if (AHEAD) w[AHEAD ? i : 0] = weight(i);
-    }
-    int row = blockIdx.x;
-    fetch(row);
-    for (int turn = 0; row < a.rows; row += gridDim.x, turn ^= 1) {
+        for (int i = 0; i < NV; ++i) w[AHEAD ? i : 0] = weight(i);
+    const int step = gridDim.x * groups;
+    int row = blockIdx.x * groups + group;
+    if (row < a.rows) fetch(row);
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
         const float rstd = rn;
         float g[NV][8], xh[NV][8], dot = 0.f;
-        int4 ds[NV];
+        int4 d[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float wf[8];
             unpack8<E>(sn[i], xh[i]);
             unpack8<E>(yn[i], g[i]);
             unpack8<E>(AHEAD ? w[AHEAD ? i : 0] : weight(i), wf);
-            ds[i] = dn[i];
+            d[i] = dn[i];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 xh[i][j] *= rstd;
@@ -200,25 +205,45 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
                 dot = fmaf(g[i][j], xh[i][j], dot);
             }
         }
-        const bool more = gridDim.x < a.rows - row;
-        if (AHEAD && more) fetch(row + gridDim.x);
-        dot = block_total(dot, red[turn]) / (float)a.hidden;
+        const bool more = step < a.rows - row;
+        if (AHEAD && more) fetch(row + step);
+        dot = warp_total(dot);
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = dot;
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(th) : "memory");
+            dot = 0.f;
+            for (int i = 0; i < warps; ++i) dot += red[turn][w0 + i];
+        }
+        dot /= (float)a.hidden;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
+            const int c = i * th + tid;
             if (c >= vecs) continue;
             float o[8];
-            if (a.dsum && !AHEAD) ds[i] = ld_stream(static_cast<const E*>(a.dsum) + row * a.ld_dsum + 8 * c);
-            unpack8<E>(ds[i], o);  // zeros without dsum
+            unpack8<E>(d[i], o);  // zeros without dsum
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, g[i][j] - xh[i][j] * dot, o[j]);
             store8(static_cast<E*>(a.dx) + (size_t)row * a.hidden + 8 * c, true, 8, o);
         }
-        if (!AHEAD && more) fetch(row + gridDim.x);
+        if (!AHEAD && more) fetch(row + step);
+    }
+    if (NV == 1 && groups > 1) {
+        for (int g = 0; g < groups; ++g) {
+            if (group == g && tid < vecs) {
+                float* at = share + 8 * tid;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (g) dw[0][j] += at[j];
+                    at[j] = dw[0][j];
+                }
+            }
+            __syncthreads();
+        }
+        if (group != groups - 1) return;  // the last group holds the sum
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = i * blockDim.x + threadIdx.x;
+        const int c = i * th + tid;
         if (c < vecs) store8_f32(a.partial + (size_t)blockIdx.x * a.hidden + 8 * c, true, 8, dw[i]);
     }
 }
@@ -329,13 +354,22 @@ cudaError_t norm(const NormArgs& a, cudaStream_t st) {
 }
 template <typename E>
 cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
-    const int nv = row_vectors(a.hidden), th = row_threads(a.hidden, nv), nb = norm_bwd_blocks(a.rows);
+    const int nv = row_vectors(a.hidden), th = row_threads(a.hidden, nv);
+    // rows that share a block: as many as its threads allow, 15 barriers and
+    // (half of the threads, so that their gradients fit) shared memory
+    int groups = nv == 1 && th <= kMostThreads / 2 ? kMostThreads / th : 1;
+    if (groups > 15) groups = 15;
+    if (groups > a.rows) groups = a.rows > 0 ? a.rows : 1;
+    const int nb = a.rows ? (a.rows + groups - 1) / groups < norm_bwd_blocks(a.rows) ? (a.rows + groups - 1) / groups
+                                                                                     : norm_bwd_blocks(a.rows)
+                          : 0;
     if (nb) {
+        const dim3 grid(nb), block(th * groups);
         cudaError_t e;
-        if (nv == 1) e = launch_pdl(rms_norm_bwd_kernel<E, 1>, dim3(nb), dim3(th), 0, st, a);
-        else if (nv == 2) e = launch_pdl(rms_norm_bwd_kernel<E, 2>, dim3(nb), dim3(th), 0, st, a);
-        else if (nv == 8) e = launch_pdl(rms_norm_bwd_kernel<E, 8>, dim3(nb), dim3(th), 0, st, a);
-        else e = launch_pdl(rms_norm_bwd_kernel<E, 4>, dim3(nb), dim3(th), 0, st, a);
+        if (nv == 1) e = launch_pdl(rms_norm_bwd_kernel<E, 1>, grid, block, 0, st, a, groups);
+        else if (nv == 2) e = launch_pdl(rms_norm_bwd_kernel<E, 2>, grid, block, 0, st, a, groups);
+        else if (nv == 4) e = launch_pdl(rms_norm_bwd_kernel<E, 4>, grid, block, 0, st, a, groups);
+        else e = launch_pdl(rms_norm_bwd_kernel<E, 8>, grid, block, 0, st, a, groups);
         if (e) return e;
     }
     return column_total<E>(a.partial, nb, a.hidden, a.dw, st);
