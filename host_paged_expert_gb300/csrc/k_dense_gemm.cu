@@ -171,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 2 * TN);
     tc::fence_before_sync();
     __syncthreads();
-    tc::cluster_arrive();
+    tc::cluster_arrive_relaxed();
     tc::cluster_wait();
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
@@ -372,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    tc::cluster_arrive();
+    tc::cluster_arrive_relaxed();
     tc::cluster_wait();
     tc::fence_after_sync();
     if (warp == 2) tc::tmem_dealloc_pair(tmem, 2 * TN);

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     else reduce<E, KIND, 8>(p.e, ring, q.nt, rank, t0, f0);
     // no CTA leaves while another may read its partial
     if (q.split > 1) {
-        tc::cluster_arrive();
+        tc::cluster_arrive_relaxed();
         tc::cluster_wait();
     }
     tc::fence_after_sync();
