@@ -96,7 +96,10 @@ int split_blocks(const SplitShape& s, int kb);
 // CTAs of this shape that the current device holds at once.
 int split_resident(const SplitShape& s);
 
-using PFN_encode = PFN_cuTensorMapEncodeTiled_v12000;
+// Tensor map of an operand of `rows` rows and depth k: boxes of 128 bytes
+// along K by box_rows rows, or (mn: stored [k, rows]) of 64 rows by 64 along
+// K, swizzled over 128 bytes.
+bool encode_operand(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8, int box_rows);
 
 struct NormArgs {
     const void *x, *res, *w;

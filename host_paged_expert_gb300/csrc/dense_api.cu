@@ -269,6 +269,7 @@ extern "C" pe_status pe_gated_ffn(const void* x, int64_t x_stride, const void* w
         Product p = make(x, x_stride, 0, w13, hidden, 0, rows, 2 * intermediate, hidden);
         p.e.cols = intermediate;
         p.e.act = act;
+        // h is rounded to 16 bits, the type that the second product's MMA takes
         p.e.out = workspace;
         p.e.ld_out = intermediate;
         p.e.keep = keep;
@@ -322,6 +323,10 @@ extern "C" pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, co
     void* dgu = ws;
     void* h = ws + up256(4 * (size_t)rows * intermediate);
     const int64_t I2 = 2 * (int64_t)intermediate;
+    // dg, du and h are rounded to 16 bits, the type that the next products' MMAs
+    // take, and so were the kept gate and up, half the memory of fp32: together
+    // the gradients are off by twice their own rounding (bf16: 3.5e-3 instead
+    // of 1.7e-3 in the 2-norm), independent per element.
     if (!e) {
         Product p = make(dy, dy_stride, 0, w2, intermediate, 1, rows, intermediate, hidden);
         p.e.act = act;

