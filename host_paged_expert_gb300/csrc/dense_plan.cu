@@ -1,8 +1,8 @@
 // Which kernel and which tiles a matrix product takes: the least of the
 // times that these models give.  They were fitted to GB300 measurements of
-// both kernels (70 plain bf16 products of 8 to 2048 rows, operands in L2, in
-// microseconds), agree with them to 8 % and choose a shape 1 % slower than
-// the best one on average:
+// both kernels (94 plain bf16 products of 8 to 2048 rows, operands in L2, in
+// microseconds), agree with them to 8 % and choose a shape 1 to 2 % slower
+// than the best one on average:
 //
 //   rows x K x cols   CTA pairs, 256 / 128 columns   cluster split (tokens, CTAs along K)
 //   8 x 2048 x 2048        13.3 / 9.8                 9.8 (16, 1)   6.8 (16, 2)   5.0 (16, 4)   4.5 (16, 8)
@@ -11,6 +11,8 @@
 //   400 x 8192 x 1024      39.4 / 29.5               34.8 (64, 1)  20.7 (64, 2)  17.8 (64, 4)  15.9 (128, 4)
 //   1024 x 2048 x 2048     14.2 / 11.1               14.1 (64, 1)  21.2 (64, 2)  37.0 (64, 4)  13.2 (128, 1)
 //   2048 x 4096 x 4096     41.0 / 57.4               87.5 (64, 1)
+//   16 x 2048 x 12288                                7.8 (16, 2)   7.65 (16, 3) 11.5 (16, 4)
+//   300 x 6144 x 2048                               21.5 (64, 2)  17.2 (64, 3)  24.1 (64, 4)
 //
 //   rows x K x cols   warps streaming weights        best cluster split
 //   1 x 4096 x 2048         2.7                       5.2
@@ -51,25 +53,29 @@ double pair_time(const Product& p, EpiKind kind, int tn) {
     return c.fixed + c.full * std::min(1.0, p.M / 256.0) + waves * kb * c.block + (waves - 1) * std::max(0.0, c.epi - kb * c.block);
 }
 
-// The same with the K blocks of one CTA, or all weights from HBM; blocks on
-// one SM share its tensor core; partial sums cross the cluster.
+// The same with the K blocks of one CTA, or all weights from HBM (L2 where
+// they may stay there); two CTAs on an SM, which some SMs have as soon as
+// there are more than one each, take half as long again; partial sums cross
+// the cluster.
 double split_time(const Product& p, EpiKind kind, const SplitShape& s) {
     const bool fp8 = p.a_scale != nullptr;
     const int kb = up(p.K, fp8 ? 128 : 64), share = up(kb, s.split);
     const double base = (double)up(p.e.cols, kind == EPI_GATED ? 64 : 128) * up(p.M, s.nt), ctas = base * s.split;
-    const double block = fp8 ? 0.27 + 0.0033 * s.nt : s.nt <= 64 ? 0.225 : 0.247;
+    const double block = fp8 ? 0.28 + 0.0035 * s.nt : s.nt <= 64 ? 0.24 : 0.26;
     const double slots = split_resident(s);  // fewer than the SMs hold: a cluster stays within a GPC
-    const double fixed = 2.05 + 0.0193 * s.nt, waves = std::max(1.0, std::ceil(ctas / slots));
-    const double stream = (double)p.N * p.K * (fp8 ? 1 : 2) / 6.2e6;  // the weights at HBM's rate
-    return (fixed + (s.split > 1 ? 0.55 : 0.0)) * waves + std::max(stream, share * block * std::max(1.0, 1.06 * ctas / kSms)) +
-           base * s.nt * 512.0 * (s.split - 1) / 2.1e6 + 0.05 * (s.split - 1);
+    const double fixed = 1.83 + 0.0265 * s.nt + (s.split > 1 ? 0.4 : 0.0), waves = std::max(1.0, std::ceil(ctas / slots));
+    const double shared = s.nt <= 64 && ctas / waves > slots / 2 ? 1.47 : 1.0;
+    const double bytes = (double)p.N * p.K * (fp8 ? 1 : 2), stream = bytes / (bytes > 64e6 ? 6.2e6 : 11e6);
+    return fixed * waves + std::max(stream, share * block * shared * waves) + base * s.nt * 512.0 * (s.split - 1) / 1.7e6 +
+           0.055 * (s.split - 1);
 }
 
-// Weights at what HBM and L2 gave, or the multiply-adds with operands from L1.
+// Weights at what HBM and L2 gave, less with each further row; or the
+// multiply-adds with operands from L1.
 double gemv_time(const Product& p) {
     const bool fp8 = p.a_scale != nullptr;
     const double weights = (double)p.N * p.K;
-    return 1.7 + std::max(weights * (fp8 ? 1 : 2) / 7.2e6, p.M * weights / (fp8 ? 5.0e6 : 6.3e6));
+    return 1.7 + std::max(weights * (fp8 ? 1 : 2) / 7.2e6 * (1 + 0.3 * (p.M - 1)), p.M * weights / (fp8 ? 5.0e6 : 6.3e6));
 }
 
 // The best kernel for one product and its time.
@@ -96,7 +102,7 @@ Choice choose(const Product& p, EpiKind kind) {
         SplitShape s;
         const int tiles = up(p.M, most);
         s.nt = up(up(p.M, tiles), 16) * 16;
-        for (s.split = 1; s.split <= 8 && s.split <= kb; s.split *= 2) {
+        for (s.split = 1; s.split <= 8 && s.split <= kb; ++s.split) {
             const double us = split_time(p, kind, s);
             const bool fits = !f32 || fp8 || split_blocks(s, kb) <= 8;
             if (fits > bounded || (fits == bounded && us < c.us)) c.us = us, c.tn = 0, c.shape = s, bounded = fits;

@@ -13,9 +13,9 @@
 // a part of the tile, in rank order, so the result does not depend on timing,
 // needs no workspace and no second launch.
 //
-// What bounds it: a K block of 64 takes 0.225 us whatever the tokens (four
-// MMAs of 128 rows), a launch 2 us and 0.02 us per token of the tile, and the
-// partials cross the cluster at 2 TB/s: 8 x 2048 to 128 with fp32 results 3.7
+// What bounds it: a K block of 64 takes 0.24 us whatever the tokens (four
+// MMAs of 128 rows), a launch 2 us and 0.026 us per token of the tile, and the
+// partials cross the cluster at 1.7 TB/s: 8 x 2048 to 128 with fp32 results 3.7
 // us, 64 x 2048 to 2048 5.7 us, 64 x 4096 to 4096 9.2 us (floor 4.9).
 //
 // The second product of a feed-forward block starts early: it loads its
@@ -62,16 +62,17 @@ struct Shared {
 // order, and applies the epilogue.  Each thread asks for all the parts of
 // several units before it adds the first: the round trip to another SM's
 // shared memory is paid once.
+// split: CTAs of the cluster, at most SPLIT.
 template <typename E, int KIND, int SPLIT>
-__device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt, int rank, int t0, int f0) {
+__device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt, int split, int rank, int t0, int f0) {
     constexpr int NF = KIND == EPI_GATED ? kRows / 2 : kRows, U = NF / 8, G = KIND == EPI_GATED ? 2 : 1;
     constexpr int BATCH = 4 / (SPLIT * G) > 1 ? 4 / (SPLIT * G) : 1;
     // each rank takes whole rows, as many as the others
-    const int rows = min(nt, e.rows - t0), mine = (rows + SPLIT - 1) / SPLIT, r0 = rank * mine;
+    const int rows = min(nt, e.rows - t0), mine = (rows + split - 1) / split, r0 = rank * mine;
     const int total = min(mine, rows - r0) * U;
     uint32_t from[SPLIT];
 #pragma unroll
-    for (int r = 0; r < SPLIT; ++r) from[r] = tc::map_rank(tc::smem_u32(ring), r);
+    for (int r = 0; r < SPLIT; ++r) from[r] = tc::map_rank(tc::smem_u32(ring), r < split ? r : 0);
     // the stride between a thread's units is a multiple of U: its columns stay the same
     const int u0 = (int)threadIdx.x, col = f0 + (u0 % U) * 8;
     float bias[8];
@@ -85,24 +86,23 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
             const uint32_t at = (uint32_t)(t * kRows + (u0 % U) * 8) * 4;
             in[i] = epi_load<E, KIND>(e, u < total ? t0 + t : e.rows, col);
             if (u >= total) continue;
-            float4 a[G][SPLIT][2];
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+            for (int g = 0; g < G; ++g) {
+                float4 a[SPLIT][2];
 #pragma unroll
                 for (int r = 0; r < SPLIT; ++r)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) a[g][r][h] = tc::ld_cluster_f4(from[r] + at + g * NF * 4 + h * 16);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
+                    for (int h = 0; h < 2; ++h)
+                        if (SPLIT <= 2 || r < split) a[r][h] = tc::ld_cluster_f4(from[r] + at + g * NF * 4 + h * 16);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][g][j] = 0.f;
 #pragma unroll
                 for (int r = 0; r < SPLIT; ++r)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float4 x = a[g][r][h];
+                        if (SPLIT > 2 && r >= split) continue;
                         float* d = v[i][g] + 4 * h;
-                        d[0] += x.x, d[1] += x.y, d[2] += x.z, d[3] += x.w;
+                        d[0] += a[r][h].x, d[1] += a[r][h].y, d[2] += a[r][h].z, d[3] += a[r][h].w;
                     }
             }
         }
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ---- the tile's sum over the cluster, and the epilogue
-    if (q.split == 1) reduce<E, KIND, 1>(p.e, ring, q.nt, rank, t0, f0);
-    else if (q.split == 2) reduce<E, KIND, 2>(p.e, ring, q.nt, rank, t0, f0);
-    else if (q.split == 4) reduce<E, KIND, 4>(p.e, ring, q.nt, rank, t0, f0);
-    else reduce<E, KIND, 8>(p.e, ring, q.nt, rank, t0, f0);
+    if (q.split == 1) reduce<E, KIND, 1>(p.e, ring, q.nt, 1, rank, t0, f0);
+    else if (q.split == 2) reduce<E, KIND, 2>(p.e, ring, q.nt, 2, rank, t0, f0);
+    else if (q.split <= 4) reduce<E, KIND, 4>(p.e, ring, q.nt, q.split, rank, t0, f0);
+    else reduce<E, KIND, 8>(p.e, ring, q.nt, q.split, rank, t0, f0);
     // no CTA leaves while another may read its partial
     if (q.split > 1) {
         tc::cluster_arrive_relaxed();
@@ -399,7 +399,7 @@ cudaError_t launch(const Product& p, const SplitShape& s, int chain, uint32_t* e
     q.sub_len = (share + q.subs - 1) / q.subs;
     q.cols = 32;
     while (q.cols < (q.nt + 31) / 32 * 32 + q.nt * (q.subs - 1)) q.cols *= 2;
-    if (q.cols > tmem_cols(s.nt) || kall < s.split || s.nt > (FP8 ? 64 : 128)) return cudaErrorInvalidValue;
+    if (q.cols > tmem_cols(s.nt) || kall < s.split || s.split > 8 || s.nt > (FP8 ? 64 : 128)) return cudaErrorInvalidValue;
     constexpr int NF = KIND == EPI_GATED ? kRows / 2 : kRows;
     q.ftiles = (p.e.cols + NF - 1) / NF;
     const long long blocks = (long long)q.ftiles * ((p.M + s.nt - 1) / s.nt) * s.split;
@@ -439,8 +439,8 @@ int split_blocks(const SplitShape& s, int kb) {
 }
 
 int split_resident(const SplitShape& s) {
-    static std::atomic<int> known[2][4];  // one or two blocks per SM; 1, 2, 4 or 8 CTAs along K
-    const int two = s.nt <= kPairTokens, at = s.split >= 8 ? 3 : s.split >= 4 ? 2 : s.split - 1;
+    static std::atomic<int> known[2][9];  // one or two blocks per SM; CTAs along K
+    const int two = s.nt <= kPairTokens, at = s.split;
     int n = known[two][at].load();
     if (n) return n;
     n = 152;  // where the runtime does not say
