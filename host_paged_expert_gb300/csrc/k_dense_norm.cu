@@ -15,7 +15,9 @@ namespace {
 // Threads of a row block: one vector of 8 each, more where a row has over 512
 // vectors.  (16384 x 4096 with an 8-bit output: 97 us with up to 512 threads,
 // 102 us with 256, 135 us with 128; 8192 x 8192 without: 85, 114, 114 us.)
-constexpr int kMostThreads = 512;
+// Rows of over 1024 vectors take up to 1024 threads: at 64 registers each a
+// block fills the SM (4096 x 9000: 75 us, 99 us with 288 threads).
+constexpr int kMostThreads = 512, kWideThreads = 1024;
 
 __device__ __forceinline__ float warp_total(float v) {
 #pragma unroll
@@ -56,54 +58,63 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // A block takes rows b, b + gridDim, ...: NV vectors of 8 elements per thread,
 // held in registers between the sum of squares and the output; the next row's
 // loads are in flight meanwhile.  The norm is taken of the fp32 sum, before it
-// is rounded for the residual stream.
-template <typename E, int NV>
-__global__ void __launch_bounds__(kMostThreads, NV <= 2 ? 2 : 1) rms_norm_kernel(const NormArgs a) {
+// is rounded for the residual stream.  RAW: rows of more than 8192 columns are
+// held as they were read, and each vector of the next row is asked for as soon
+// as this row's is used up (2048 x 32768: 99 us, 5400 GB/s; 107 us with the
+// fp32 values in registers; 4096 x 16384 106 and 123 us).
+template <typename E, int NV, bool RAW>
+__global__ void __launch_bounds__(RAW ? kWideThreads : kMostThreads, RAW ? 1 : 2) rms_norm_kernel(const NormArgs a) {
     __shared__ float red[2][32];
     pdl_wait();
     const int vecs = a.hidden >> 3;
-    constexpr int NW = NV <= 2 ? NV : 1;  // weights stay in registers where there is room
+    constexpr int NW = RAW ? 1 : NV;  // weights stay in registers where there is room
     int4 xn[NV], rn[NV], w[NW];
     auto weight = [&](int i) {
         const int c = i * blockDim.x + threadIdx.x;
         return c < vecs ? *reinterpret_cast<const int4*>(static_cast<const E*>(a.w) + 8 * c) : make_int4(0, 0, 0, 0);
     };
+    auto fetch1 = [&](int row, int i) {
+        const int c = i * blockDim.x + threadIdx.x;
+        if (c < vecs) {
+            xn[i] = ld_stream(static_cast<const E*>(a.x) + row * a.ld_x + 8 * c);
+            if (a.res) rn[i] = ld_stream(static_cast<const E*>(a.res) + row * a.ld_res + 8 * c);
+        }
+    };
     auto fetch = [&](int row) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            if (c < vecs) {
-                xn[i] = ld_stream(static_cast<const E*>(a.x) + row * a.ld_x + 8 * c);
-                if (a.res) rn[i] = ld_stream(static_cast<const E*>(a.res) + row * a.ld_res + 8 * c);
+        for (int i = 0; i < NV; ++i) fetch1(row, i);
+    };
+    // the sum that is normed, of vector i
+    auto value = [&](int i, float (&o)[8]) {
+        if (i * blockDim.x + threadIdx.x < vecs) {
+            unpack8<E>(xn[i], o);
+            if (a.res) {
+                float t[8];
+                unpack8<E>(rn[i], t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] += t[j];
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0.f;
         }
     };
     int row = blockIdx.x;
     fetch(row);
 #pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = weight(i);
+    for (int i = 0; i < NW; ++i)
+        if (!RAW) w[i] = weight(i);
     for (int turn = 0; row < a.rows; row += gridDim.x, turn ^= 1) {
-        float v[NV][8], ss = 0.f;
+        float keep[RAW ? 1 : NV][8], ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            if (c < vecs) {
-                unpack8<E>(xn[i], v[i]);
-                if (a.res) {
-                    float t[8];
-                    unpack8<E>(rn[i], t);
+            float(&v)[8] = keep[RAW ? 0 : i];
+            value(i, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] += t[j];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
         }
         const bool more = gridDim.x < a.rows - row;
-        if (NV <= 4 && more) fetch(row + gridDim.x);
+        if (!RAW && more) fetch(row + gridDim.x);
         ss = block_total(ss, red[turn]);
         const float rstd = rsqrtf(ss / (float)a.hidden + a.eps);
         if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
@@ -112,15 +123,20 @@ __global__ void __launch_bounds__(kMostThreads, NV <= 2 ? 2 : 1) rms_norm_kernel
         for (int i = 0; i < NV; ++i) {
             const int c = i * blockDim.x + threadIdx.x;
             const bool in = c < vecs;
-            if (in && a.sum) store8(static_cast<E*>(a.sum) + base + 8 * c, true, 8, v[i]);
+            float(&v)[8] = keep[RAW ? 0 : i];
+            if (RAW) {
+                value(i, v);
+                if (more) fetch1(row + gridDim.x, i);
+            }
+            if (in && a.sum) store8(static_cast<E*>(a.sum) + base + 8 * c, true, 8, v);
             float wf[8], top = 0.f;
-            unpack8<E>(NW == NV ? w[i < NW ? i : 0] : weight(i), wf);
+            unpack8<E>(RAW ? weight(i) : w[RAW ? 0 : i], wf);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[i][j] = in ? v[i][j] * rstd * wf[j] : 0.f;
-                top = max_nan(top, fabsf(v[i][j]));
+                v[j] = in ? v[j] * rstd * wf[j] : 0.f;
+                top = max_nan(top, fabsf(v[j]));
             }
-            if (in && a.y) store8(static_cast<E*>(a.y) + base + 8 * c, true, 8, v[i]);
+            if (in && a.y) store8(static_cast<E*>(a.y) + base + 8 * c, true, 8, v);
             if (a.codes) {  // sixteen threads hold the 128 features of one scale
 #pragma unroll
                 for (int o = 8; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -134,9 +150,9 @@ __global__ void __launch_bounds__(kMostThreads, NV <= 2 ? 2 : 1) rms_norm_kernel
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                            make_float2(v[i][4 * h] * inv, v[i][4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                            make_float2(v[4 * h] * inv, v[4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
                         const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                            make_float2(v[i][4 * h + 2] * inv, v[i][4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+                            make_float2(v[4 * h + 2] * inv, v[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
                         q[h] = lo | (hi << 16);
                     }
                     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.codes) + base + 8 * c) = make_uint2(q[0], q[1]);
@@ -145,7 +161,6 @@ __global__ void __launch_bounds__(kMostThreads, NV <= 2 ? 2 : 1) rms_norm_kernel
                 }
             }
         }
-        if (NV > 4 && more) fetch(row + gridDim.x);  // no registers for it earlier
     }
 }
 
@@ -153,10 +168,9 @@ __global__ void __launch_bounds__(kMostThreads, NV <= 2 ? 2 : 1) rms_norm_kernel
 // Every group keeps its share of the weight's gradient in registers, the
 // groups' shares are added in order through shared memory and written once
 // to partial[block].  The next row's loads are in flight while a row is
-// reduced (NV <= 2, where there are registers for it).
+// reduced.
 template <typename E, int NV>
 __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a, int groups) {
-    constexpr bool AHEAD = NV <= 2;
     __shared__ float red[2][32];
     __shared__ float share[NV == 1 ? 8 * kMostThreads / 2 : 1];
     pdl_wait();
@@ -182,10 +196,9 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
         const int c = i * th + tid;
         return c < vecs ? *reinterpret_cast<const int4*>(static_cast<const E*>(a.w) + 8 * c) : make_int4(0, 0, 0, 0);
     };
-    int4 w[AHEAD ? NV : 1];
-    if (AHEAD)
+    int4 w[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) w[AHEAD ? i : 0] = weight(i);
+    for (int i = 0; i < NV; ++i) w[i] = weight(i);
     const int step = gridDim.x * groups;
     int row = blockIdx.x * groups + group;
     if (row < a.rows) fetch(row);
@@ -198,7 +211,7 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
             float wf[8];
             unpack8<E>(sn[i], xh[i]);
             unpack8<E>(yn[i], g[i]);
-            unpack8<E>(AHEAD ? w[AHEAD ? i : 0] : weight(i), wf);
+            unpack8<E>(w[i], wf);
             d[i] = dn[i];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -208,8 +221,7 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
                 dot = fmaf(g[i][j], xh[i][j], dot);
             }
         }
-        const bool more = step < a.rows - row;
-        if (AHEAD && more) fetch(row + step);
+        if (step < a.rows - row) fetch(row + step);
         dot = warp_total(dot);
         if (warps > 1) {
             if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = dot;
@@ -228,7 +240,6 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
             for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, g[i][j] - xh[i][j] * dot, o[j]);
             store8(static_cast<E*>(a.dx) + (size_t)row * a.hidden + 8 * c, true, 8, o);
         }
-        if (!AHEAD && more) fetch(row + step);
     }
     if (NV == 1 && groups > 1) {
         for (int g = 0; g < groups; ++g) {
@@ -248,6 +259,89 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
     for (int i = 0; i < NV; ++i) {
         const int c = i * th + tid;
         if (c < vecs) store8_f32(a.partial + (size_t)blockIdx.x * a.hidden + 8 * c, true, 8, dw[i]);
+    }
+}
+
+// The same for rows of more than 8192 columns, whose fp32 values no longer
+// fit: the row is held as it was read, the block's share of the weight's
+// gradient lies in shared memory (each thread its own columns, so that no
+// barrier is needed), and each vector of the next row is asked for as soon as
+// this row's is used up.  2048 x 32768: 128 us, 4180 GB/s (402 us with the
+// fp32 values in 128 registers of 512 threads, which spilled).
+template <typename E, int NV>
+__global__ void __launch_bounds__(kWideThreads, 1) rms_norm_bwd_wide_kernel(const NormBwdArgs a) {
+    extern __shared__ float4 dw[];  // the first halves of all vectors, then the second ones
+    __shared__ float red[2][32];
+    pdl_wait();
+    const int vecs = a.hidden >> 3;
+    int4 sn[NV], yn[NV], dn[NV];
+    auto fetch1 = [&](int row, int i) {
+        const int c = i * blockDim.x + threadIdx.x;
+        if (c < vecs) {
+            sn[i] = ld_stream(static_cast<const E*>(a.sum) + row * a.ld_sum + 8 * c);
+            yn[i] = ld_stream(static_cast<const E*>(a.dy) + row * a.ld_dy + 8 * c);
+            if (a.dsum) dn[i] = ld_stream(static_cast<const E*>(a.dsum) + row * a.ld_dsum + 8 * c);
+        }
+    };
+    int row = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * blockDim.x + threadIdx.x;
+        sn[i] = yn[i] = dn[i] = make_int4(0, 0, 0, 0);
+        fetch1(row, i);
+        if (c < vecs) dw[c] = dw[vecs + c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int turn = 0; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const float rstd = a.rstd[row];
+        // dy * w and sum * rstd of vector i; dyx: the weight's gradient of this row
+        auto parts = [&](int i, int c, float (&g)[8], float (&xh)[8], float (&dyx)[8]) {
+            float wf[8];
+            unpack8<E>(sn[i], xh);
+            unpack8<E>(yn[i], g);
+            unpack8<E>(*reinterpret_cast<const int4*>(static_cast<const E*>(a.w) + 8 * c), wf);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                xh[j] *= rstd;
+                dyx[j] = g[j] * xh[j];
+                g[j] *= wf[j];
+            }
+        };
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            if (c >= vecs) continue;
+            float g[8], xh[8], dyx[8];
+            parts(i, c, g, xh, dyx);
+            float4 lo = dw[c], hi = dw[vecs + c];
+            lo.x += dyx[0], lo.y += dyx[1], lo.z += dyx[2], lo.w += dyx[3];
+            hi.x += dyx[4], hi.y += dyx[5], hi.z += dyx[6], hi.w += dyx[7];
+            dw[c] = lo, dw[vecs + c] = hi;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot = fmaf(g[j], xh[j], dot);
+        }
+        dot = block_total(dot, red[turn]) / (float)a.hidden;
+        const bool more = gridDim.x < a.rows - row;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            if (c >= vecs) continue;
+            float g[8], xh[8], dyx[8], o[8];
+            parts(i, c, g, xh, dyx);
+            unpack8<E>(dn[i], o);  // zeros without dsum
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, g[j] - xh[j] * dot, o[j]);
+            if (more) fetch1(row + gridDim.x, i);
+            store8(static_cast<E*>(a.dx) + (size_t)row * a.hidden + 8 * c, true, 8, o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * blockDim.x + threadIdx.x;
+        if (c >= vecs) continue;
+        const float4 lo = dw[c], hi = dw[vecs + c];
+        const float t[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        store8_f32(a.partial + (size_t)blockIdx.x * a.hidden + 8 * c, true, 8, t);
     }
 }
 
@@ -334,11 +428,8 @@ cudaError_t column_total(const float* partial, int n, int cols, void* out, cudaS
 }
 
 int row_threads(int hidden, int nv) { return (((hidden / 8 + nv - 1) / nv) + 31) / 32 * 32; }
-int row_vectors(int hidden) {
-    int nv = 1;
-    while (nv < 8 && row_threads(hidden, nv) > kMostThreads) nv *= 2;
-    return nv;
-}
+bool wide_row(int hidden) { return hidden > 2 * 8 * kMostThreads; }
+int row_vectors(int hidden) { return row_threads(hidden, 1) <= kMostThreads ? 1 : row_threads(hidden, 2) <= kWideThreads ? 2 : 4; }
 constexpr int kSms = 152;
 // Threads per SM that the forward pass's grid counts on: with the next row
 // always on its way these keep HBM busy, and more only make the last rows
@@ -350,10 +441,18 @@ cudaError_t norm(const NormArgs& a, cudaStream_t st) {
     const int nv = row_vectors(a.hidden), th = row_threads(a.hidden, nv);
     // as many blocks as fit, and no more: a block's next row is then always on its way
     const int fit = kSms * (kResident / th > 0 ? kResident / th : 1), nb = a.rows < fit ? a.rows : fit;
-    if (nv == 1) return launch_pdl(rms_norm_kernel<E, 1>, dim3(nb), dim3(th), 0, st, a);
-    if (nv == 2) return launch_pdl(rms_norm_kernel<E, 2>, dim3(nb), dim3(th), 0, st, a);
-    if (nv == 8) return launch_pdl(rms_norm_kernel<E, 8>, dim3(nb), dim3(th), 0, st, a);
-    return launch_pdl(rms_norm_kernel<E, 4>, dim3(nb), dim3(th), 0, st, a);
+    if (nv == 4) return launch_pdl(rms_norm_kernel<E, 4, true>, dim3(nb), dim3(th), 0, st, a);
+    if (wide_row(a.hidden)) return launch_pdl(rms_norm_kernel<E, 2, true>, dim3(nb), dim3(th), 0, st, a);
+    if (nv == 2) return launch_pdl(rms_norm_kernel<E, 2, false>, dim3(nb), dim3(th), 0, st, a);
+    return launch_pdl(rms_norm_kernel<E, 1, false>, dim3(nb), dim3(th), 0, st, a);
+}
+template <typename E, int NV>
+cudaError_t norm_bwd_wide(const NormBwdArgs& a, int th, int nb, cudaStream_t st) {
+    const size_t smem = (size_t)a.hidden * sizeof(float);  // at most 128 KB: one block per SM
+    if (cudaError_t e = cudaFuncSetAttribute(rms_norm_bwd_wide_kernel<E, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             8 * kWideThreads * NV * (int)sizeof(float)))
+        return e;
+    return launch_pdl(rms_norm_bwd_wide_kernel<E, NV>, dim3(nb), dim3(th), smem, st, a);
 }
 template <typename E>
 cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
@@ -363,16 +462,15 @@ cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
     int groups = nv == 1 && th <= kMostThreads / 2 ? kMostThreads / th : 1;
     if (groups > 15) groups = 15;
     if (groups > a.rows) groups = a.rows > 0 ? a.rows : 1;
-    const int nb = a.rows ? (a.rows + groups - 1) / groups < norm_bwd_blocks(a.rows) ? (a.rows + groups - 1) / groups
-                                                                                     : norm_bwd_blocks(a.rows)
-                          : 0;
+    const int most = wide_row(a.hidden) ? kSms : norm_bwd_blocks(a.rows), want = (a.rows + groups - 1) / groups;
+    const int nb = want < most ? want : most;
     if (nb) {
         const dim3 grid(nb), block(th * groups);
         cudaError_t e;
-        if (nv == 1) e = launch_pdl(rms_norm_bwd_kernel<E, 1>, grid, block, 0, st, a, groups);
+        if (nv == 4) e = norm_bwd_wide<E, 4>(a, th, nb, st);
+        else if (wide_row(a.hidden)) e = norm_bwd_wide<E, 2>(a, th, nb, st);
         else if (nv == 2) e = launch_pdl(rms_norm_bwd_kernel<E, 2>, grid, block, 0, st, a, groups);
-        else if (nv == 4) e = launch_pdl(rms_norm_bwd_kernel<E, 4>, grid, block, 0, st, a, groups);
-        else e = launch_pdl(rms_norm_bwd_kernel<E, 8>, grid, block, 0, st, a, groups);
+        else e = launch_pdl(rms_norm_bwd_kernel<E, 1>, grid, block, 0, st, a, groups);
         if (e) return e;
     }
     return column_total<E>(a.partial, nb, a.hidden, a.dw, st);

@@ -104,6 +104,15 @@ def test_rms_norm_backward(D, rows, h, dt, add):
     assert same(dx, again[0]) and same(dw, again[1])
 
 
+@pytest.mark.parametrize("rows,h", [(500, 8200), (333, 16376), (320, 32768)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_rms_norm_wide(D, rows, h, dt):
+    """Rows wider than registers hold, several to a block."""
+    test_rms_norm(D, rows, h, dt, True)
+    test_rms_norm_backward(D, rows, h, dt, False)
+    test_rms_norm_backward(D, rows, h, dt, True)
+
+
 def test_rms_norm_strides(D):
     x, r, w, dy = rand(9, 264), rand(9, 264, seed=1), rand(264, seed=2), rand(9, 264, seed=3)
     a, b = D.rms_norm(x, w, r, save=True), D.rms_norm(pitched(x, 8), w, pitched(r, 24), save=True)
