@@ -130,10 +130,10 @@ struct ActBwdArgs {
     void* dz;
     int64_t ld_dz;
     void* db;
-    float* partial;  // [act_bwd_chunks(rows)][cols], when db is not NULL
+    float* partial;  // [act_bwd_chunks(rows, cols)][cols], when db is not NULL
     int act, rows, cols;
 };
-int act_bwd_chunks(int rows);
+int act_bwd_chunks(int rows, int cols);
 cudaError_t launch_act_bwd(const ActBwdArgs& a, int elem, cudaStream_t st);
 
 #ifdef __CUDACC__

@@ -122,20 +122,21 @@ cudaError_t launch_choice(const Choice& c, const Product& p, EpiKind kind, int e
     return launch_split(p, kind, elem, c.shape, chain, err, st);
 }
 
-// Products of 16-bit operands in one launch: the pair with the most K blocks.
+// Products of 16-bit operands in one launch: the busiest pair, whose tiles
+// take their K blocks or their epilogue, whichever is longer.
 double group_time(const Product* p, int count, int tn) {
+    const PairCost& c = tn == 256 ? kWide : kNarrow;
     double load[(int)kPairs] = {};
     long long t = 0;
     for (int i = 0; i < count; ++i) {
         const long long n = (long long)up(p[i].M, 256) * up(p[i].e.cols, tn);
-        const double kb = up(p[i].K, 64), whole = (double)(n / (int)kPairs) * kb;
+        const double kb = up(p[i].K, 64), tile = std::max(kb * c.block, c.epi), whole = (double)(n / (int)kPairs) * tile;
         for (int j = 0; j < (int)kPairs; ++j)
-            load[j] += whole + (((j - t) % (int)kPairs + (int)kPairs) % (int)kPairs < n % (int)kPairs ? kb : 0);
+            load[j] += whole + (((j - t) % (int)kPairs + (int)kPairs) % (int)kPairs < n % (int)kPairs ? tile : 0);
         t += n;
     }
     const double most = *std::max_element(load, load + (int)kPairs);
-    const PairCost& c = tn == 256 ? kWide : kNarrow;
-    return c.fixed + c.full + most * c.block;
+    return c.fixed + c.full + most;
 }
 
 }  // namespace
