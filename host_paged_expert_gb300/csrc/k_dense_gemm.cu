@@ -44,7 +44,9 @@ namespace dense {
 
 namespace {
 
-constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 2 TMEM, 4..11 epilogue
+// Epilogue warps (warps 4 and on; warp 0 TMA, 1 MMA, 2 TMEM).
+constexpr int epi_warps(int kind, bool fp8, int tn) { return fp8 || kind == EPI_GATED || tn == 256 ? 8 : 16; }
+constexpr int threads(int kind, bool fp8, int tn) { return 128 + 32 * epi_warps(kind, fp8, tn); }
 constexpr int kTile = 256;             // rows of C per CTA pair
 constexpr int kHalf = 128;             // of which each CTA has these
 constexpr int kOperand = kHalf * 128;  // bytes of A's stage in one CTA
@@ -54,11 +56,13 @@ constexpr int kMaxStages = 8;
 // TN: columns of C per pair (of gate and up together), 256 or 128.
 constexpr int patch_bytes(int kind) { return kind == EPI_GATED ? 8192 : 4096; }
 constexpr int stage_bytes(int tn) { return kOperand + tn / 2 * 128; }
-constexpr int stages(int kind, int tn) {
-    const int n = (225 * 1024 - 8 * patch_bytes(kind)) / stage_bytes(tn);
+constexpr int stages(int kind, bool fp8, int tn) {
+    const int n = (225 * 1024 - epi_warps(kind, fp8, tn) * patch_bytes(kind)) / stage_bytes(tn);
     return n < kMaxStages ? n : kMaxStages;
 }
-constexpr int smem_bytes(int kind, int tn) { return 1024 + stages(kind, tn) * stage_bytes(tn) + 8 * patch_bytes(kind); }
+constexpr int smem_bytes(int kind, bool fp8, int tn) {
+    return 1024 + stages(kind, fp8, tn) * stage_bytes(tn) + epi_warps(kind, fp8, tn) * patch_bytes(kind);
+}
 
 // Registers: 128 x (72 + 2 x 216) = 384 x 168, what the block is launched with.
 constexpr int kRegsFew = 72, kRegsMany = 216;
@@ -122,6 +126,19 @@ __device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, in
     });
 }
 
+// x / d and x % d without a division: the product with 2^32 / d, rounded down,
+// is the quotient or one less.
+struct Divide {
+    uint32_t d, inv;
+    static Divide by(uint32_t d) { return {d, d > 1 ? (uint32_t)((uint64_t(1) << 32) / d) : 0xffffffffu}; }
+    __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t& rest) const {
+        uint32_t q = __umulhi(x, inv);
+        rest = x - q * d;
+        if (rest >= d) rest -= d, ++q;
+        return q;
+    }
+};
+
 // Products that one launch computes: their tiles are dealt out to the pairs
 // as one sequence, so that a product's last wave is filled by the next one's
 // tiles.
@@ -130,6 +147,7 @@ struct Work {
     CUtensorMap a[N], b[N];
     Product p[N];
     int tiles[N];
+    Divide across[N];  // by a product's tiles along its columns
     int count;
 };
 
@@ -142,21 +160,24 @@ struct Walk {
         while (i < w.count && t - base >= w.tiles[i]) base += w.tiles[i++];
         return i < w.count;
     }
-    // row and column of the tile in its product: kRaster tile rows at a time
-    __device__ __forceinline__ void at(const Product& p, int cols, int& m, int& n) const {
-        const int tm = (p.M + kTile - 1) / kTile, tn = (p.e.cols + cols - 1) / cols;
-        const int per = kRaster * tn, first = (t - base) / per * kRaster, rows = min(kRaster, tm - first), r = (t - base) % per;
-        m = first + r % rows;
-        n = r / rows;
+    // row and column of the tile in its product: kRaster tile rows at a time,
+    // down each column of them
+    __device__ __forceinline__ void at(const Product& p, const Divide& across, int& m, int& n) const {
+        const int tm = (p.M + kTile - 1) / kTile, x = t - base;
+        uint32_t r;
+        const int first = (int)across((uint32_t)x / kRaster, r) * kRaster, rows = min(kRaster, tm - first);
+        const uint32_t in = r * kRaster + x % kRaster;  // of the tile among the group's
+        n = (int)(rows == kRaster ? in / kRaster : in / rows);
+        m = first + (int)(in - n * rows);
     }
 };
 
 // NP: products that the launch may hold.  With one, its fields are constants
 // of the instructions; found by index they cost 5 % of a large product's time.
 template <typename E, int KIND, bool FP8, int TN, int NP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, TN), 1)
     pair_kernel(const __grid_constant__ Work<NP> work, uint32_t* err) {
-    constexpr int STAGES = stages(KIND, TN), kStage = stage_bytes(TN);
+    constexpr int STAGES = stages(KIND, FP8, TN), kStage = stage_bytes(TN);
     constexpr int BK = FP8 ? 128 : 64;                      // elements of a 128-byte row
     constexpr int NT = KIND == EPI_GATED ? TN / 2 : TN;  // result columns of a tile
     extern __shared__ uint8_t dyn[];
@@ -174,7 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&S.acc_full[i], 1);
-            tc::mbar_init(&S.acc_empty[i], 16);  // eight epilogue warps of each CTA
+            tc::mbar_init(&S.acc_empty[i], 2 * epi_warps(KIND, FP8, TN));  // of both CTAs
         }
         tc::mbar_init(&S.drain, 1);
         tc::fence_barrier_init();
@@ -204,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const CUtensorMap &ta = work.a[NP == 1 ? 0 : walk.i], &tb = work.b[NP == 1 ? 0 : walk.i];
                 const int kblocks = (p.K + BK - 1) / BK;
                 int mt, nt;
-                walk.at(p, NT, mt, nt);
+                walk.at(p, work.across[NP == 1 ? 0 : walk.i], mt, nt);
                 const int m0 = mt * kTile + (int)rank * kHalf;
                 const int n0 = KIND == EPI_GATED ? (int)rank * p.e.cols + nt * NT : nt * NT + (int)rank * (TN / 2);
                 for (int kb = 0; kb < kblocks; ++kb) {
@@ -288,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Product& p = work.p[NP == 1 ? 0 : walk.i];
             const int kblocks = (p.K + BK - 1) / BK;
             int mt, nt;
-            walk.at(p, NT, mt, nt);
+            walk.at(p, work.across[NP == 1 ? 0 : walk.i], mt, nt);
             const int row0 = mt * kTile + (int)rank * kHalf + quarter * 32;
             if (FP8) {
                 uint64_t acc[4][16];  // pairs of fp32
@@ -348,18 +369,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             } else {
                 const uint32_t buf = use_acc & 1;
+                constexpr int SHARE = epi_warps(KIND, FP8, TN) / 4;  // warps that share a tile's columns
                 Ahead<E, KIND> x;
-                x.load(p.e, lane, row0, nt * NT + half * (NT / 2));
+                x.load(p.e, lane, row0, nt * NT + half * (NT / SHARE));
                 if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
                 ++use_acc;
                 tc::fence_after_sync();
-                constexpr int CH = NT / 64;  // 32-column chunks of this warp's half
-                const int c0 = half * (NT / 2);
+                constexpr int CH = NT / SHARE / 32;  // 32-column chunks of this warp's share
+                const int c0 = half * (NT / SHARE);
                 const uint32_t at = lanes + buf * TN + c0;
 #pragma unroll 1
                 for (int c = 0; c < CH; ++c) {
-                    Ahead<E, KIND> n;
-                    if (c + 1 < CH) n.load(p.e, lane, row0, nt * NT + c0 + (c + 1) * 32);
                     uint32_t r[32];
                     tc::tmem_ld32(at + c * 32, r);
                     tc::tmem_ld_wait();
@@ -376,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     patch_out<E, KIND>(p.e, patch, lane, row0, nt * NT + c0 + c * 32, x);
-                    x = n;
+                    if (c + 1 < CH) x.load(p.e, lane, row0, nt * NT + c0 + (c + 1) * 32);
                 }
             }
         }
@@ -400,11 +420,11 @@ cudaError_t resident_pairs(int* out) {
     int n = dev < 64 ? known[dev].load() : 0;
     if (!n) {
         auto k = pair_kernel<E, KIND, FP8, TN, NP>;
-        if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND, TN))) return e;
+        if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND, FP8, TN))) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem_bytes(KIND, TN);
+        cfg.blockDim = dim3(threads(KIND, FP8, TN));
+        cfg.dynamicSmemBytes = smem_bytes(KIND, FP8, TN);
         if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) return e;
         if (n < 1) return cudaErrorLaunchOutOfResources;
         if (dev < 64) known[dev].store(n);
@@ -428,11 +448,12 @@ cudaError_t launch(const Product* p, int count, uint32_t* err, cudaStream_t st) 
         const long long n = (long long)((p[i].M + kTile - 1) / kTile) * ((p[i].e.cols + NT - 1) / NT);
         if ((tiles += n) > INT_MAX / 2) return cudaErrorInvalidValue;
         w.tiles[i] = (int)n;
+        w.across[i] = Divide::by((p[i].e.cols + NT - 1) / NT);
     }
     int pairs = 0;
     if (cudaError_t e = resident_pairs<E, KIND, FP8, TN, NP>(&pairs)) return e;
     if (tiles < pairs) pairs = (int)tiles;
-    return launch_pdl(pair_kernel<E, KIND, FP8, TN, NP>, dim3(2 * pairs), dim3(kThreads), smem_bytes(KIND, TN), st, w, err);
+    return launch_pdl(pair_kernel<E, KIND, FP8, TN, NP>, dim3(2 * pairs), dim3(threads(KIND, FP8, TN)), smem_bytes(KIND, FP8, TN), st, w, err);
 }
 
 template <typename E>
