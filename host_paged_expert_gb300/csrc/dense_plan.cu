@@ -1,16 +1,19 @@
 // Which kernel and which tiles a matrix product takes: the least of the
 // times that these models give.  They were fitted to GB300 measurements of
-// both kernels (94 plain bf16 products of 8 to 2048 rows, operands in L2, in
-// microseconds), agree with them to 8 % and choose a shape 1 to 2 % slower
-// than the best one on average:
+// both kernels (94 plain bf16 products of 8 to 2048 rows and 60 of 512 to 8192
+// on CTA pairs, operands in L2, in microseconds), agree with them to 8 % and 3
+// % and choose a shape 1 to 2 % slower than the best one on average:
 //
 //   rows x K x cols   CTA pairs, 256 / 128 columns   cluster split (tokens, CTAs along K)
 //   8 x 2048 x 2048        13.3 / 9.8                 9.8 (16, 1)   6.8 (16, 2)   5.0 (16, 4)   4.5 (16, 8)
 //   64 x 4096 x 4096       22.1 / 16.5               18.8 (64, 1)  12.4 (64, 2)   9.5 (64, 4)  11.9 (64, 8)
-//   256 x 2048 x 2048      14.1 / 10.5               11.1 (64, 1)   8.7 (64, 2)  10.2 (64, 4)  20.4 (64, 8)
+//   256 x 2048 x 2048      13.8 / 9.9                11.1 (64, 1)   8.7 (64, 2)  10.2 (64, 4)  20.4 (64, 8)
 //   400 x 8192 x 1024      39.4 / 29.5               34.8 (64, 1)  20.7 (64, 2)  17.8 (64, 4)  15.9 (128, 4)
 //   1024 x 2048 x 2048     14.2 / 11.1               14.1 (64, 1)  21.2 (64, 2)  37.0 (64, 4)  13.2 (128, 1)
 //   2048 x 4096 x 4096     41.0 / 57.4               87.5 (64, 1)
+//   8192 x 256 x 4096      24.4 / 22.0
+//   4096 x 512 x 4096      18.1 / 18.3
+//   4096 x 1024 x 4096     23.9 / 29.2
 //   16 x 2048 x 12288                                7.8 (16, 2)   7.65 (16, 3) 11.5 (16, 4)
 //   300 x 6144 x 2048                               21.5 (64, 2)  17.2 (64, 3)  24.1 (64, 4)
 //
@@ -36,11 +39,27 @@ int up(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Of a launch of CTA pairs: starting it, filling the pipeline and the last
 // tile's epilogue (`full` of it for tiles with all their rows); a K block of
-// a tile; and what of a tile's epilogue shows if its K blocks are short.
+// a tile; what each further tile costs beyond its K blocks; and how often one
+// can follow another where K is short, a plain epilogue and some of its K
+// blocks.  `heavier`: what `epi_extra` takes, against tiles of 128 columns.
 struct PairCost {
-    double fixed, full, block, epi;
+    double fixed, full, block, gap, epi, slope, heavier;
 };
-constexpr PairCost kWide = {4.8, 1.1, 0.264, 1.75}, kNarrow = {3.4, 0.45, 0.219, 0.93};  // 256, 128 columns
+constexpr PairCost kWide = {5.2, 0.1, 0.265, 0.5, 2.65, 0.11, 2.7}, kNarrow = {3.15, 0.45, 0.205, 0.42, 1.25, 0.03, 1.0};
+
+// What a linear epilogue does besides converting and storing (8192 x 256 to
+// 8192, 27 tiles of 128 columns a pair: plain 39 us, gelu_tanh 61, bias and
+// residual 68, gelu_tanh with its input kept 73, all of it 101); narrow tiles
+// of gate and up have half the epilogue warps.
+double epi_extra(const Product& p, EpiKind kind, int tn) {
+    if (kind == EPI_GATED) return tn == 128 ? 0.7 : 0.0;
+    if (kind != EPI_LINEAR) return 0;
+    return (p.e.act != PE_ACT_NONE ? 0.8 : 0.0) + (p.e.bias ? 0.2 : 0.0) + (p.e.res ? 0.9 : 0.0) + (p.e.keep ? 0.5 : 0.0);
+}
+
+double tile_time(const PairCost& c, int kb, double extra) {
+    return std::max(kb * c.block + c.gap, c.epi + kb * c.slope + c.heavier * extra);
+}
 
 // 8-bit operands: every tile's epilogue is exposed (its warps add up the K
 // blocks), 3.3 us.
@@ -50,7 +69,9 @@ double pair_time(const Product& p, EpiKind kind, int tn) {
     const double waves = std::max(1.0, std::ceil((double)up(p.M, 256) * up(p.e.cols, cols) / kPairs));
     if (fp8) return 3.0 + waves * (kb * 0.45 + 3.3);
     const PairCost& c = tn == 256 ? kWide : kNarrow;
-    return c.fixed + c.full * std::min(1.0, p.M / 256.0) + waves * kb * c.block + (waves - 1) * std::max(0.0, c.epi - kb * c.block);
+    const double extra = epi_extra(p, kind, tn);
+    return c.fixed + (c.full + c.heavier * extra) * std::min(1.0, p.M / 256.0) + kb * c.block +
+           (waves - 1) * tile_time(c, kb, extra);
 }
 
 // The same with the K blocks of one CTA, or all weights from HBM (L2 where
@@ -130,7 +151,7 @@ double group_time(const Product* p, int count, int tn) {
     long long t = 0;
     for (int i = 0; i < count; ++i) {
         const long long n = (long long)up(p[i].M, 256) * up(p[i].e.cols, tn);
-        const double kb = up(p[i].K, 64), tile = std::max(kb * c.block, c.epi), whole = (double)(n / (int)kPairs) * tile;
+        const double tile = tile_time(c, up(p[i].K, 64), 0), whole = (double)(n / (int)kPairs) * tile;
         for (int j = 0; j < (int)kPairs; ++j)
             load[j] += whole + (((j - t) % (int)kPairs + (int)kPairs) % (int)kPairs < n % (int)kPairs ? tile : 0);
         t += n;

@@ -1,16 +1,16 @@
 // Matrix products of the dense operators: C[m, n] = sum_k A(m, k) B(n, k),
 // then the epilogue.
 //
-// pair_kernel: persistent CTA pairs (two SMs), 256 x 256 tiles of C.  Each
-// CTA's TMA producer streams its half of A and of B (128 rows x 128 bytes
-// each, 128-byte swizzle) into a ring of stages; one thread of the pair's
-// leader issues the 256 x 256 tcgen05.mma, which reads both CTAs' shared
-// memory, so a byte of B feeds 256 rows instead of 128.  Accumulators live in
-// TMEM, two buffers of 256 columns, so that eight epilogue warps drain one
-// tile while the next is multiplied.  Each epilogue warp turns its 32 x 32
-// blocks through a swizzled shared-memory patch, after which eight lanes hold
-// eight rows' 64 contiguous bytes and every load and store of the epilogue is
-// coalesced.
+// pair_kernel: persistent CTA pairs (two SMs), 256 x 256 tiles of C (or 256 x
+// 128, below).  Each CTA's TMA producer streams its half of A and of B (128
+// rows x 128 bytes each, 128-byte swizzle) into a ring of stages; one thread
+// of the pair's leader issues the 256 x 256 tcgen05.mma, which reads both
+// CTAs' shared memory, so a byte of B feeds 256 rows instead of 128.
+// Accumulators live in TMEM, two buffers of 256 columns, so that the epilogue
+// warps drain one tile while the next is multiplied.  Each epilogue warp turns
+// its 32 x 32 blocks through a swizzled shared-memory patch, after which eight
+// lanes hold eight rows' 64 contiguous bytes and every load and store of the
+// epilogue is coalesced.
 //
 // Operands may be row-major along K or along M / N (the backward products
 // read the same tensors transposed): both have a swizzled layout that the
@@ -21,10 +21,13 @@
 //
 // Bound by the tensor cores: bf16 8192^3 561 us (1960 TFLOP/s), 4096^3 78 us
 // with the tensor pipe active 89 % of the cycles; 256 tiles fill 76 pairs'
-// four waves to 84 %.  Where K is short the epilogue shows: a 256 x 256 tile
-// takes 1.7 us more with its K blocks than the 264 ns that each of them
-// costs (4864 x 1024 x 4096: 25.5 us plain, 28.9 with SiLU, 38.9 with bias,
-// GELU and residual).
+// four waves to 84 %.  Where K is short the epilogue shows, and that is bound
+// by instruction issue: with eight warps a 256 x 256 tile takes 2.9 us at K =
+// 128, when its K blocks take 0.53.  So tiles of 256 x 128 columns, the choice
+// for short K and heavy epilogues, have sixteen epilogue warps (8192 x 256 to
+// 8192 39 us, with gelu_tanh 61, with bias, residual and kept values too 101;
+// eight: 53, 84, 148); in tiles of 256 columns their patches cost a stage
+// (4096^3 2 % slower), gate and up would need twice the patches.
 //
 // E4M3 operands: a stage is 128 deep, one scale group.  Each stage's product
 // goes to its own TMEM buffer and the epilogue warps add it, times the row's
