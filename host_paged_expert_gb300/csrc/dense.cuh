@@ -133,6 +133,9 @@ struct ActBwdArgs {
     float* partial;  // [act_bwd_chunks(rows, cols)][cols], when db is not NULL
     int act, rows, cols;
 };
+// Chunks are of kSumRows rows or more, so that one row of column sums for every
+// kSumRows rows of dy is always enough room for `partial`, whatever the chunk.
+constexpr int kSumRows = 32;
 int act_bwd_chunks(int rows, int cols);
 cudaError_t launch_act_bwd(const ActBwdArgs& a, int elem, cudaStream_t st);
 

@@ -165,14 +165,15 @@ extern "C" pe_status pe_linear(const void* x, int64_t x_stride, const float* x_s
 
 namespace {
 // pe_linear_backward's workspace: dz with rows padded to 8 elements, then the
-// column sums' partials.
+// column sums' partials, whose room goes by the sizes alone (the chunk that
+// the kernel takes is a matter of speed, and no caller's).
 size_t dz_bytes(int rows, int n) { return up256(2 * (size_t)rows * pad8(n)); }
 }  // namespace
 
 extern "C" size_t pe_linear_backward_workspace(int32_t rows, int32_t out_features, int32_t act) {
     if (rows <= 0 || out_features <= 0 || !is_act(act)) return 0;
     const size_t dz = act != PE_ACT_NONE || out_features % 8 ? dz_bytes(rows, out_features) : 0;
-    return dz + up256(sizeof(float) * (size_t)act_bwd_chunks(rows, out_features) * out_features);
+    return dz + up256(sizeof(float) * (((size_t)rows + kSumRows - 1) / kSumRows) * out_features);
 }
 
 extern "C" pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,

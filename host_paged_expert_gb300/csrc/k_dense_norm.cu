@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(1024) column_total_kernel(const float* partial
 // there are more than 16 blocks per SM, so that the chunks' column sums (fp32)
 // stay a small part of the traffic.
 constexpr int kActThreads = 256, kActBatch = 4;
+static_assert(kActThreads / 32 * kActBatch >= kSumRows, "a chunk has at least kSumRows rows");
 int act_vx(int cols) {
     int vx = 1;
     while (vx < 32 && 8 * vx < cols) vx *= 2;

@@ -421,7 +421,10 @@ pe_status pe_linear(const void* x, int64_t x_stride, const float* x_scale, const
  *   dx = dz weight [rows, in], dweight = dz^T x [out, in], dbias = column
  *   sums of dz [out]; each may be NULL.  The residual's gradient is dy.
  * keep may be NULL for PE_ACT_NONE.
- * workspace: pe_linear_backward_workspace(rows, out, act) bytes. */
+ * workspace: pe_linear_backward_workspace(rows, out, act) bytes: dz where it
+ *   is not dy itself (act, or out no multiple of 8: rows of out rounded up to
+ *   8 elements), and one fp32 row of `out` sums for every 32 rows begun, each
+ *   rounded up to 256 bytes. */
 size_t pe_linear_backward_workspace(int32_t rows, int32_t out_features, int32_t act);
 pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
                              const void* keep, int32_t act, void* dx, void* dweight, void* dbias, void* workspace,
