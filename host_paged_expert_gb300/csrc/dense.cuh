@@ -23,6 +23,11 @@ namespace dense {
 
 constexpr int kGroup = 128;  // features sharing one scale of an 8-bit row; rows and columns of a weight block
 
+// Rows are counted in int.  A loop over rows steps past the last one by its
+// launch's stride, at most 4864 rows, and sizes are rounded up to a tile or a
+// chunk, at most 4096 rows: PE_MAX_ROWS leaves 65535 below INT_MAX.
+static_assert(INT_MAX - PE_MAX_ROWS == 65535, "room for a stride past the last row");
+
 // What a matrix product does with its accumulators before they are stored.
 enum EpiKind {
     EPI_LINEAR = 0,     // act(v + bias) + residual; optionally v + bias is kept

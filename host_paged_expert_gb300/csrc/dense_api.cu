@@ -89,6 +89,7 @@ extern "C" pe_status pe_rms_norm(const void* x, int64_t x_stride, const void* re
     if (!is_elem(elem)) return bad("pe_rms_norm: elem must be PE_ELEM_BF16 or PE_ELEM_F16");
     if (rows < 0 || hidden < 8 || hidden % 8) return bad("pe_rms_norm: hidden must be a positive multiple of 8, rows not negative");
     if (hidden > kMaxNormHidden) return bad("pe_rms_norm: hidden above 32768", PE_ERR_RANGE);
+    if (rows > PE_MAX_ROWS) return bad("pe_rms_norm: more than PE_MAX_ROWS rows", PE_ERR_RANGE);
     if (rows == 0) return PE_OK;
     if (!x || !weight) return bad("pe_rms_norm: NULL pointer");
     if (!codes != !scales) return bad("pe_rms_norm: codes and scales go together");
@@ -113,6 +114,7 @@ extern "C" pe_status pe_rms_norm_backward(const void* dy, int64_t dy_stride, con
     if (rows < 0 || hidden < 8 || hidden % 8)
         return bad("pe_rms_norm_backward: hidden must be a positive multiple of 8, rows not negative");
     if (hidden > kMaxNormHidden) return bad("pe_rms_norm_backward: hidden above 32768", PE_ERR_RANGE);
+    if (rows > PE_MAX_ROWS) return bad("pe_rms_norm_backward: more than PE_MAX_ROWS rows", PE_ERR_RANGE);
     if (!dweight || (rows && (!dy || !sum || !weight || !rstd || !dx))) return bad("pe_rms_norm_backward: NULL pointer");
     const size_t need = pe_rms_norm_backward_workspace(rows, hidden);
     if (workspace_bytes < need || (need && !workspace)) return bad("pe_rms_norm_backward: workspace too small");
@@ -138,6 +140,7 @@ extern "C" pe_status pe_linear(const void* x, int64_t x_stride, const float* x_s
     if (rows < 0 || out_features < 1 || in_features < 16 / bytes || in_features * (int64_t)bytes % 16)
         return bad("pe_linear: in_features must be a positive multiple of 8 (of 16 for E4M3), out_features positive");
     if (in_features > kMaxFeatures || out_features > kMaxFeatures) return bad("pe_linear: more than 2^24 features", PE_ERR_RANGE);
+    if (rows > PE_MAX_ROWS) return bad("pe_linear: more than PE_MAX_ROWS rows", PE_ERR_RANGE);
     if (rows == 0) return PE_OK;
     if (!x || !weight || !out) return bad("pe_linear: NULL pointer");
     if (!aligned(x) || !aligned(weight) || !aligned(bias) || !aligned(residual) || !aligned(out) || !aligned(keep))
@@ -186,6 +189,7 @@ extern "C" pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const
         return bad("pe_linear_backward: in_features must be a positive multiple of 8, out_features positive");
     if (in_features > kMaxFeatures || out_features > kMaxFeatures)
         return bad("pe_linear_backward: more than 2^24 features", PE_ERR_RANGE);
+    if (rows > PE_MAX_ROWS) return bad("pe_linear_backward: more than PE_MAX_ROWS rows", PE_ERR_RANGE);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (rows == 0) {
         cudaError_t e = dweight ? cudaMemsetAsync(dweight, 0, 2 * (size_t)out_features * in_features, st) : cudaSuccess;
@@ -256,6 +260,7 @@ extern "C" pe_status pe_gated_ffn(const void* x, int64_t x_stride, const void* w
     if (rows < 0 || hidden < 8 || hidden % 8 || intermediate < 8 || intermediate % 8)
         return bad("pe_gated_ffn: hidden and intermediate must be positive multiples of 8");
     if (hidden > kMaxFeatures || intermediate > kMaxFeatures) return bad("pe_gated_ffn: more than 2^24 features", PE_ERR_RANGE);
+    if (rows > PE_MAX_ROWS) return bad("pe_gated_ffn: more than PE_MAX_ROWS rows", PE_ERR_RANGE);
     if (rows == 0) return PE_OK;
     if (!x || !w13 || !w2 || !out) return bad("pe_gated_ffn: NULL pointer");
     if (workspace_bytes < pe_gated_ffn_workspace(rows, intermediate) || !workspace) return bad("pe_gated_ffn: workspace too small");
@@ -303,6 +308,7 @@ extern "C" pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, co
         return bad("pe_gated_ffn_backward: hidden and intermediate must be positive multiples of 8");
     if (hidden > kMaxFeatures || intermediate > kMaxFeatures)
         return bad("pe_gated_ffn_backward: more than 2^24 features", PE_ERR_RANGE);
+    if (rows > PE_MAX_ROWS) return bad("pe_gated_ffn_backward: more than PE_MAX_ROWS rows", PE_ERR_RANGE);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const size_t wbytes = 2 * (size_t)hidden * intermediate;
     if (rows == 0) {

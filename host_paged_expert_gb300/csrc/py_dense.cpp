@@ -80,7 +80,7 @@ void pitched(Ten& t, const char* name) {
     if (t.d0 <= 1) t.s0 = t.d1;
 }
 
-// Rows and features are 32-bit in the C ABI.
+// Features are 32-bit in the C ABI.
 void fits(int64_t v) {
     if (v > INT32_MAX) bad(PE_ERR_RANGE, "a dimension of %lld is too large", (long long)v);
 }
@@ -89,7 +89,7 @@ void fits(int64_t v) {
 Ten matrix(PyObject* o, const char* name) {
     Ten t = load(o, name);
     if (t.nd != 2) bad(PE_ERR_INVALID, "%s: want a matrix [rows, features], got %d-d", name, (int)t.nd);
-    fits(t.d0);
+    if (t.d0 > PE_MAX_ROWS) bad(PE_ERR_RANGE, "%s: a number of rows of %lld is too large, at most %d", name, (long long)t.d0, PE_MAX_ROWS);
     fits(t.d1);
     pitched(t, name);
     return t;

@@ -355,7 +355,8 @@ pe_status pe_expert_mlp_noalloc(const void* w13, const void* w2, const void* x, 
  *     residual instead).  Outputs may not overlap inputs or each other.
  *   - Sums, norms and accumulators are fp32; a result is rounded to its type
  *     once, when it is stored.
- *   - rows = 0 is a no-op, except that weight gradients are then set to zero.
+ *   - rows = 0 is a no-op, except that weight gradients are then set to zero;
+ *     more than PE_MAX_ROWS are refused (PE_ERR_RANGE).
  *   - Results do not depend on timing: the same call gives the same bits.
  *   - Errors: PE_ERR_INVALID (NULL, misaligned, bad sizes or types),
  *     PE_ERR_RANGE (above a stated limit), PE_ERR_CUDA; the message is in
@@ -376,6 +377,10 @@ typedef enum pe_act {
 
 /* Features that share one scale of an 8-bit row. */
 #define PE_SCALE_GROUP 128
+
+/* Most rows of a call: the kernels count rows in 32 bits, up to a launch's
+ * stride past the last one. */
+#define PE_MAX_ROWS 2147418112 /* 2^31 - 2^16 */
 
 /* RMS norm of x + residual:
  *   s = x + residual (x alone if residual is NULL),

@@ -33,3 +33,39 @@ def test_linear_backward_workspace_goes_by_the_sizes(L, rows, out, act):
 def test_linear_backward_workspace_of_nothing(L):
     assert L.pe_linear_backward_workspace(0, 64, 1) == L.pe_linear_backward_workspace(4, 0, 1) == 0
     assert L.pe_linear_backward_workspace(4, 64, 5) == 0
+
+
+# ---- rows past what the kernels' 32-bit counters hold
+
+A = 1 << 20  # an aligned address that no refused call uses
+MOST = (1 << 31) - (1 << 16)
+N = None
+CALLS = {  # at `rows` rows of 64 features, 32 outputs
+    "pe_rms_norm": lambda r: (A, 64, A, 64, A, 1e-6, A, A, A, A, A, r, 64, 0, N),
+    "pe_rms_norm_backward": lambda r: (A, 64, A, 64, A, 64, A, A, A, A, A, 1 << 60, r, 64, 0, N),
+    "pe_linear": lambda r: (A, 64, N, A, N, A, A, 32, A, 0, A, 1, r, 64, 32, 0, N),
+    "pe_linear_backward": lambda r: (A, 32, A, 64, A, A, 1, A, A, A, A, 1 << 60, r, 64, 32, 0, N),
+    "pe_gated_ffn": lambda r: (A, 64, A, A, A, 64, A, A, 1, A, 1 << 60, r, 64, 32, 0, N),
+    "pe_gated_ffn_backward": lambda r: (A, 64, A, 64, A, A, A, 1, A, A, A, A, 1 << 60, r, 64, 32, 0, N),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("rows", [MOST + 1, (1 << 31) - 4863, (1 << 31) - 1])
+def test_too_many_rows(L, name, rows):
+    assert getattr(L, name)(*CALLS[name](rows)) == _lib.PE_ERR_RANGE
+    assert b"PE_MAX_ROWS" in L.pe_last_error(None)
+
+
+def test_too_many_rows_from_python():
+    torch = pytest.importorskip("torch")
+    from host_paged_expert_gb300 import dense
+
+    row = torch.zeros(1, 64, dtype=torch.bfloat16)
+    x, w, w13, w2 = row.expand(MOST + 1, 64), row.expand(24, 64).contiguous(), row.expand(32, 64).contiguous(), torch.zeros(64, 16, dtype=row.dtype)
+    for call in (lambda: dense.rms_norm(x, row[0]), lambda: dense.linear(x, w), lambda: dense.gated_ffn(x, w13, w2)):
+        with pytest.raises(_lib.PEError, match="too large") as e:
+            call()
+        assert e.value.status == _lib.PE_ERR_RANGE
+    with pytest.raises(_lib.PEError, match="want CUDA tensors"):  # the most rows are not refused
+        dense.linear(row.expand(MOST, 64), w)
