@@ -78,6 +78,17 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// Waits for this thread's loads from TMEM and hands their registers on: named
+// here, no use of them can be moved ahead of the wait (an instruction that the
+// compiler does not know to write them).
+template <int N, int... M>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N], uint32_t (&... more)[M]) {
+    if constexpr (sizeof...(more) > 0) tmem_ld_wait(more...);
+    else tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // One MMA over a CTA pair (PAIR) or one CTA; FP8: E4M3 operands, 32 deep,
 // else 16-bit operands, 16 deep.
 template <bool PAIR, bool FP8>

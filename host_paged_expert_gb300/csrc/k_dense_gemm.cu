@@ -344,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                         uint32_t r[2][32];
                         tc::tmem_ld32(at + h * 64, r[0]);
                         tc::tmem_ld32(at + h * 64 + 32, r[1]);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld_wait(r[0], r[1]);
                         if (h == 1) {
                             tc::fence_before_sync();
                             if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
@@ -385,12 +385,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                 for (int c = 0; c < CH; ++c) {
                     uint32_t r[32];
                     tc::tmem_ld32(at + c * 32, r);
-                    tc::tmem_ld_wait();
+                    tc::tmem_ld_wait(r);
                     __syncwarp();  // the patch's last readers are done
                     patch_put(patch, lane, r);
                     if (KIND == EPI_GATED) {
                         tc::tmem_ld32(at + TN / 2 + c * 32, r);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld_wait(r);
                         patch_put(patch + 4096, lane, r);
                     }
                     if (c == CH - 1) {

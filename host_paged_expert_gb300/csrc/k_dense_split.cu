@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (c * 32 < q.nt) {
                         uint32_t r[32];
                         tc::tmem_ld32(lanes + buf * q.nt + c * 32, r);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld_wait(r);
 #pragma unroll
                         for (int n = 0; n < 32; ++n)
                             acc[c][n] = fmaf(__uint_as_float(r[n]), __shfl_sync(0xffffffffu, xs[c], n), acc[c][n]);
@@ -308,26 +308,30 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
             if (tc::mbar_spin(&S.acc_full[0], 0, err)) {
                 tc::fence_after_sync();
-                // the next chunk is on its way while this one is stored
-                uint32_t r[32], n[32];
+                // the next chunk is on its way while this one is stored; two arrays in turn
+                uint32_t r[2][32];
                 const int last = (nkb - 1) / q.sub_len;  // accumulators 0..last hold parts
-                tc::tmem_ld32(lanes, r);
-                for (int c = 0; c < q.nt; c += 32) {
-                    tc::tmem_ld_wait();
-                    for (int b = 1; b <= last; ++b) {
-                        tc::tmem_ld32(lanes + b * q.nt + c, n);
-                        tc::tmem_ld_wait();
+                tc::tmem_ld32(lanes, r[0]);
+                for (int c0 = 0; c0 < q.nt; c0 += 64) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(n[j]));
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = c0 + 32 * h;
+                        if (c >= q.nt) break;
+                        tc::tmem_ld_wait(r[h]);
+                        for (int b = 1; b <= last; ++b) {
+                            tc::tmem_ld32(lanes + b * q.nt + c, r[h ^ 1]);
+                            tc::tmem_ld_wait(r[h ^ 1]);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                r[h][j] = __float_as_uint(__uint_as_float(r[h][j]) + __uint_as_float(r[h ^ 1][j]));
+                        }
+                        if (c + 32 < q.nt) tc::tmem_ld32(lanes + c + 32, r[h ^ 1]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) part[(c + j) * kRows] = __uint_as_float(r[h][j]);
+                        if (c + 16 < q.nt)
+#pragma unroll
+                            for (int j = 16; j < 32; ++j) part[(c + j) * kRows] = __uint_as_float(r[h][j]);
                     }
-                    if (c + 32 < q.nt) tc::tmem_ld32(lanes + c + 32, n);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * kRows] = __uint_as_float(r[j]);
-                    if (c + 16 < q.nt)
-#pragma unroll
-                        for (int j = 16; j < 32; ++j) part[(c + j) * kRows] = __uint_as_float(r[j]);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = n[j];
                 }
             }
             tc::fence_before_sync();
