@@ -173,6 +173,18 @@ struct Elem<__half> {
     static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
 };
 
+// 16 bytes that are read once.  Loads of these kernels are coherent ones: a
+// block may be resident, waiting for the launch before it, while that launch
+// still writes what the block will read, and the read-only path is only for
+// memory that nothing writes as long as the kernel lives.
+__device__ __forceinline__ int4 ld_stream(const void* p) {
+    int4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // Eight consecutive elements at p[0..7].  vec: p is 16-byte aligned and all
 // eight exist; else the first n of them are touched one by one.
 template <typename E>

@@ -324,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                 const bool live = row < p.M && nt * NT + half * 128 < p.N;
                 const float* as = p.a_scale + (size_t)(live ? row : 0) * kblocks;
                 const float* bs = p.b_scale + (size_t)(live ? nb : 0) * kblocks;
-                float next = live ? __ldg(as) * __ldg(bs) : 0.f;
+                float next = live ? as[0] * bs[0] : 0.f;
                 if (p.e.res && p.e.vec && live) {  // the residual's 256 bytes on their way to L2
                     const uint8_t* rp = static_cast<const uint8_t*>(p.e.res) + 2 * (row * p.e.ld_res + nt * NT + half * 128);
 #pragma unroll
@@ -333,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                 }
                 for (int kb = 0; kb < kblocks && ok; ++kb) {
                     const uint64_t sc = tc::pack2(__float_as_uint(next), __float_as_uint(next));
-                    if (kb + 1 < kblocks && live) next = __ldg(as + kb + 1) * __ldg(bs + kb + 1);
+                    if (kb + 1 < kblocks && live) next = as[kb + 1] * bs[kb + 1];
                     const uint32_t buf = use_acc & 1, at = lanes + buf * TN + half * 128;
                     if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
                     tc::fence_after_sync();

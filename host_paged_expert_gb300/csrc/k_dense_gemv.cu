@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(const __grid_constant
             const int i = c + u * step;
             a[u] = b[u] = make_int4(0, 0, 0, 0);
             if (i < pieces) {
-                a[u] = ld_nc_na(w0 + 16 * (size_t)i);
-                b[u] = ld_nc_na(w1 + 16 * (size_t)i);
+                a[u] = ld_stream(w0 + 16 * (size_t)i);
+                b[u] = ld_stream(w1 + 16 * (size_t)i);
             }
         }
     };
@@ -103,19 +103,19 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(const __grid_constant
                     float wa[16], wb[16];
                     unpack16(a[u], wa);
                     unpack16(b[u], wb);
-                    const float sa = __ldg(p.b_scale + (size_t)(n0 / kGroup) * groups_k + g);
-                    const float sb = __ldg(p.b_scale + (size_t)(n1 / kGroup) * groups_k + g);
+                    const float sa = p.b_scale[(size_t)(n0 / kGroup) * groups_k + g];
+                    const float sb = p.b_scale[(size_t)(n1 / kGroup) * groups_k + g];
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         if (t < p.M) {
                             float xv[16], da = 0.f, db = 0.f;
-                            unpack16(__ldg(reinterpret_cast<const int4*>(x + t * p.lda + 16 * (size_t)i)), xv);
+                            unpack16(*reinterpret_cast<const int4*>(x + t * p.lda + 16 * (size_t)i), xv);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 da = fmaf(wa[j], xv[j], da);
                                 db = fmaf(wb[j], xv[j], db);
                             }
-                            const float sx = __ldg(p.a_scale + (size_t)t * groups_k + g);
+                            const float sx = p.a_scale[(size_t)t * groups_k + g];
                             acc[t][0] = fmaf(da, sa * sx, acc[t][0]);
                             acc[t][1] = fmaf(db, sb * sx, acc[t][1]);
                         }
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv_kernel(const __grid_constant
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         if (t < p.M) {
-                            const int4 xv = __ldg(reinterpret_cast<const int4*>(x + t * p.lda * ES + 16 * (size_t)i));
+                            const int4 xv = *reinterpret_cast<const int4*>(x + t * p.lda * ES + 16 * (size_t)i);
                             acc[t][0] = dot8<E>(a[u], xv, acc[t][0]);
                             acc[t][1] = dot8<E>(b[u], xv, acc[t][1]);
                         }

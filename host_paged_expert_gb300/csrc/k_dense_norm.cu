@@ -39,15 +39,6 @@ __device__ __forceinline__ float block_total(float v, float* red) {
     return t;
 }
 
-// 16 bytes that are read once
-__device__ __forceinline__ int4 ld_stream(const void* p) {
-    int4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // The larger of two magnitudes; NaN wins, so that a NaN reaches the scale.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;

@@ -273,12 +273,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             int buf = 0;
             uint32_t phase = 0;
             for (int i = 0; i < nkb; ++i) {
-                const float ws = __ldg(bs + i);
+                const float ws = bs[i];
                 float xs[2];  // the scale of this lane's token of each chunk
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int t = t0 + c * 32 + lane;
-                    xs[c] = t < p.M && c * 32 + lane < q.nt ? ws * __ldg(p.a_scale + (size_t)t * kall + kb0 + i) : 0.f;
+                    xs[c] = t < p.M && c * 32 + lane < q.nt ? ws * p.a_scale[(size_t)t * kall + kb0 + i] : 0.f;
                 }
                 if (!(ok = tc::mbar_spin(&S.acc_full[buf], phase, err))) break;
                 tc::fence_after_sync();

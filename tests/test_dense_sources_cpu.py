@@ -58,3 +58,11 @@ def test_the_rule_finds_an_early_read():
     assert early_reads("tc::tmem_ld32(a, r[1]);\nx = r[c][j];\n")
     assert not early_reads(at + "r[j] = 0;\ntc::tmem_ld_wait(n);\nr[j] = n[j];\n")
     assert not early_reads("tc::tmem_ld32(a, r[h ^ 1]);\nx = r[h][j];\ntc::tmem_ld_wait(r[h ^ 1]);\n")
+
+
+@pytest.mark.parametrize("name", KERNELS + ["dense.cuh", "dense_tc.cuh"])
+def test_loads_are_coherent(name):
+    """A block may be resident, waiting for the launch before it, while that
+    launch writes the block's inputs: the read-only path (which holds for
+    memory that nothing writes while the kernel lives) is not for them."""
+    assert not re.findall(r"__ldg|\bldg16|\bld_nc_na|\.nc\b", code(name))
