@@ -256,6 +256,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                     if (++s == STAGES) s = 0, phase ^= 1;
                 }
             }
+            // The leader's MMAs arrive on this CTA's barriers: stay until the last of
+            // them have (a stage never used passes at once).
+            for (int i = 0; ok && i < STAGES; ++i) {
+                ok = tc::mbar_spin(&S.empty[s], phase, err);
+                if (++s == STAGES) s = 0, phase ^= 1;
+            }
             // after a wait gave up: let this pair's copies land before the block ends
             if (!ok && rank == 0)
                 for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
@@ -293,6 +299,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                         if (buf == 0) buf_phase ^= 1;
                     }
                 }
+            }
+            // the other CTA's epilogue warps arrive here too: stay until the last of them have
+            for (int i = 0; ok && i < 2; ++i) {
+                ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err);
+                buf ^= 1;
+                if (buf == 0) buf_phase ^= 1;
             }
             if (!ok) {  // the MMAs already issued read shared memory and write TMEM
                 if (lead) tc::mma_commit_pair(&S.drain);
@@ -405,6 +417,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
         }
     }
     // neither CTA leaves, and no TMEM is freed, while the other may still use it
+    // (what each sends to the other's barriers was waited for above, so that
+    // the meeting has nothing to order)
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();

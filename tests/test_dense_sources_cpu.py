@@ -66,3 +66,14 @@ def test_loads_are_coherent(name):
     launch writes the block's inputs: the read-only path (which holds for
     memory that nothing writes while the kernel lives) is not for them."""
     assert not re.findall(r"__ldg|\bldg16|\bld_nc_na|\.nc\b", code(name))
+
+
+def test_pair_kernel_stays_until_the_last_arrivals():
+    """The MMAs of a pair arrive on the other CTA's `empty` barriers and its
+    epilogue warps on the leader's `acc_empty`: the meeting at the kernel's end
+    is a relaxed one, so each CTA has to have waited for what is sent to it."""
+    text = code("k_dense_gemm.cu")
+    producer, rest = text[text.index("if (warp == 0) {") :].split("} else if (warp == 1 && rank == 0) {", 1)
+    issuer = rest[: rest.index("} else {\n")]
+    assert producer.rindex("mbar_spin(&S.empty[s]") > producer.rindex("tma_load_2d_pair(")
+    assert issuer.rindex("mbar_spin(&S.acc_empty[buf]") > issuer.rindex("mma_commit_pair(&S.acc_full[buf])")
