@@ -42,7 +42,9 @@ pe_status done(cudaError_t e) {
     return bad(cudaGetErrorString(e), PE_ERR_CUDA);
 }
 
-bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned(const void* p, int to = 16) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+// what is read and written one element at a time
+bool whole(const float* p) { return aligned(p, sizeof(float)); }
 bool is_elem(int e) { return e == PE_ELEM_BF16 || e == PE_ELEM_F16; }
 bool is_act(int a) { return a >= PE_ACT_NONE && a <= PE_ACT_RELU; }
 bool pitch_ok(int64_t ld, int64_t row, int bytes) { return ld >= row && ld * bytes % 16 == 0 && ld < (int64_t(1) << 36); }
@@ -95,6 +97,7 @@ extern "C" pe_status pe_rms_norm(const void* x, int64_t x_stride, const void* re
     if (!codes != !scales) return bad("pe_rms_norm: codes and scales go together");
     if (!aligned(x) || !aligned(residual) || !aligned(weight) || !aligned(y) || !aligned(sum) || !aligned(codes))
         return bad("pe_rms_norm: pointers must be 16-byte aligned");
+    if (!whole(scales) || !whole(rstd)) return bad("pe_rms_norm: scales and rstd must be 4-byte aligned");
     if (!pitch_ok(x_stride, hidden, 2) || (residual && !pitch_ok(residual_stride, hidden, 2)))
         return bad("pe_rms_norm: row pitches must be multiples of 8 and at least hidden");
     NormArgs a = {x, residual, weight, x_stride, residual_stride, eps, y, sum, codes, scales, rstd, rows, hidden};
@@ -120,6 +123,7 @@ extern "C" pe_status pe_rms_norm_backward(const void* dy, int64_t dy_stride, con
     if (workspace_bytes < need || (need && !workspace)) return bad("pe_rms_norm_backward: workspace too small");
     if (!aligned(dy) || !aligned(dsum) || !aligned(sum) || !aligned(weight) || !aligned(dx) || !aligned(workspace))
         return bad("pe_rms_norm_backward: pointers must be 16-byte aligned");
+    if (!whole(rstd) || !aligned(dweight, 2)) return bad("pe_rms_norm_backward: rstd must be 4-byte, dweight 2-byte aligned");
     if (rows && (!pitch_ok(dy_stride, hidden, 2) || !pitch_ok(sum_stride, hidden, 2) ||
                  (dsum && !pitch_ok(dsum_stride, hidden, 2))))
         return bad("pe_rms_norm_backward: row pitches must be multiples of 8 and at least hidden");
@@ -145,6 +149,7 @@ extern "C" pe_status pe_linear(const void* x, int64_t x_stride, const float* x_s
     if (!x || !weight || !out) return bad("pe_linear: NULL pointer");
     if (!aligned(x) || !aligned(weight) || !aligned(bias) || !aligned(residual) || !aligned(out) || !aligned(keep))
         return bad("pe_linear: pointers must be 16-byte aligned");
+    if (!whole(x_scale) || !whole(w_scale)) return bad("pe_linear: scales must be 4-byte aligned");
     if (!pitch_ok(x_stride, in_features, bytes)) return bad("pe_linear: x's row pitch must be a multiple of 16 bytes and at least in_features");
     if (residual && !(out_features % 8 ? residual_stride == out_features : pitch_ok(residual_stride, out_features, 2)))
         return bad("pe_linear: residual's row pitch must be a multiple of 8 and at least out_features "
@@ -202,6 +207,7 @@ extern "C" pe_status pe_linear_backward(const void* dy, int64_t dy_stride, const
     if (workspace_bytes < need || !workspace) return bad("pe_linear_backward: workspace too small");
     if (!aligned(dy) || !aligned(x) || !aligned(weight) || !aligned(keep) || !aligned(dx) || !aligned(dweight) || !aligned(workspace))
         return bad("pe_linear_backward: pointers must be 16-byte aligned");
+    if (!aligned(dbias, 2)) return bad("pe_linear_backward: dbias must be 2-byte aligned");
     const bool odd = out_features % 8 != 0;
     if (!(odd ? dy_stride == out_features : pitch_ok(dy_stride, out_features, 2)))
         return bad("pe_linear_backward: dy's row pitch must be a multiple of 8 and at least out_features "

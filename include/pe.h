@@ -350,7 +350,8 @@ pe_status pe_expert_mlp_noalloc(const void* w13, const void* w2, const void* x, 
  *   - Matrices are row-major.  Activations that a call reads have a row
  *     pitch in elements (`*_stride`, at least the row's length); what it
  *     writes, weights and scales are contiguous.  Pointers are 16-byte
- *     aligned, pitches multiples of 16 bytes (a row length that is no
+ *     aligned (scales, rstd, pe_rms_norm_backward's dweight and dbias: as
+ *     their elements), pitches multiples of 16 bytes (a row length that is no
  *     multiple of 8, allowed for a product's outputs alone, needs a contiguous
  *     residual instead).  Outputs may not overlap inputs or each other.
  *   - Sums, norms and accumulators are fp32; a result is rounded to its type

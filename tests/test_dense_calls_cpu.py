@@ -69,3 +69,25 @@ def test_too_many_rows_from_python():
         assert e.value.status == _lib.PE_ERR_RANGE
     with pytest.raises(_lib.PEError, match="want CUDA tensors"):  # the most rows are not refused
         dense.linear(row.expand(MOST, 64), w)
+
+
+# ---- pointers to what is read or written one element at a time
+
+
+@pytest.mark.parametrize("name,at,off", [
+    ("pe_rms_norm", 9, 2), ("pe_rms_norm", 10, 1), ("pe_rms_norm", 10, 2), ("pe_rms_norm_backward", 7, 2),
+    ("pe_rms_norm_backward", 9, 1), ("pe_linear_backward", 9, 1),
+])
+def test_misaligned_elements(L, name, at, off):
+    a = list(CALLS[name](2))
+    a[at] += off
+    assert getattr(L, name)(*a) == _lib.PE_ERR_INVALID
+    assert b"byte aligned" in L.pe_last_error(None)
+
+
+@pytest.mark.parametrize("off", [(2, 0), (0, 1)])
+def test_misaligned_scales(L, off):
+    a = list(CALLS["pe_linear"](2))
+    a[2], a[4] = A + off[0], A + off[1]
+    assert L.pe_linear(*a) == _lib.PE_ERR_INVALID
+    assert b"scales must be 4-byte aligned" in L.pe_last_error(None)
