@@ -1,0 +1,119 @@
+"""Dense operators on the GPU, in the forms and at the values where a call can
+go wrong without a test of whole matrices seeing it."""
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import dense_ref as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+ACTS = ["none", "silu", "gelu", "gelu_tanh", "relu"]
+
+
+@pytest.fixture(scope="module")
+def D():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from host_paged_expert_gb300 import dense
+
+    yield dense
+    assert dense.error_word() == 0
+
+
+def rand(*shape, seed=0, scale=1.0, dt=BF):
+    g = torch.Generator(device="cuda").manual_seed(seed * 7919 + shape[0] + 31 * shape[-1])
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dt)
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ---- the activations' tails
+
+# relative error of the value and the slope at z < 0, in fp32: the argument of
+# the exponential is off by some roundings of its own size (2^-24 each; six in
+# u and its scaling, two in x log2 e), of erfc by z^2 / 2 times three, and the
+# functions themselves by 2^-21.  The slope is a sum of two such terms, of
+# which the larger is at most 1.5 times it at z <= -3.
+TAIL = {
+    "silu": lambda z: 2.0**-20 + z.abs() * 2.0**-22,
+    "gelu": lambda z: 2.0**-20 + z * z * 2.0**-22,
+    "gelu_tanh": lambda z: 2.0**-20 + 1.6 * (z.abs() + 0.045 * z.abs() ** 3) * 2.0**-21,
+}
+
+
+def tail(dt):
+    return torch.linspace(-8, -3, 640, device="cuda").to(dt)
+
+
+def exact(act, z):
+    """(act(z), act'(z)) in 64 bits, without cancellation at z < 0."""
+    z = z.double()
+    if act == "silu":
+        s = 1 / (1 + torch.exp(-z))
+        return z * s, s * (1 + z * (1 - s))
+    if act == "gelu":
+        c = 0.5 * torch.erfc(-z / math.sqrt(2))
+        return z * c, c + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    k = 2 * math.sqrt(2 / math.pi)
+    s = 1 / (1 + torch.exp(-k * (z + 0.044715 * z**3)))
+    return z * s, s + z * s * (1 - s) * k * (1 + 3 * 0.044715 * z * z)
+
+
+def through_linear(D, z, act, rows, **kw):
+    """act(z) of every value of z, as a product whose z is exact: x = z e_0,
+    weight rows e_0."""
+    x = torch.zeros(rows, 8, dtype=z.dtype, device="cuda")
+    x[:, 0] = z.repeat(-(-rows // len(z)))[:rows]
+    w = torch.zeros(16, 8, dtype=z.dtype, device="cuda")
+    w[:, 0] = 1
+    return D.linear(x, w, act=act, **kw), x[:, 0]
+
+
+TAILS = [("gelu_tanh", BF), ("gelu_tanh", HF)]
+
+
+@pytest.mark.parametrize("act,dt", TAILS)
+@pytest.mark.parametrize("rows", [1, 3, 640, 20000])
+def test_tail_of_the_activation(D, act, dt, rows):
+    y, z = through_linear(D, tail(dt), act, rows, out_dtype=F32)
+    want = exact(act, z)[0][:, None].expand(rows, 16)
+    off = (y.double() - want).abs() / want.abs()
+    assert (off <= TAIL[act](z.double())[:, None]).all(), (off / TAIL[act](z.double())[:, None]).max()
+
+
+@pytest.mark.parametrize("act,dt", TAILS)
+def test_tail_of_the_slope(D, act, dt):
+    """dbias of one row is the slope, rounded once."""
+    z = tail(dt)[None].contiguous()
+    one, w = torch.ones_like(z), torch.zeros(z.shape[1], 8, dtype=dt, device="cuda")
+    db = D.linear_backward(one, one[:, :8].contiguous(), w, z, act, bias=True)[2].double()
+    want = exact(act, z[0])[1]
+    bound = (R.U[dt] + 2 * TAIL[act](z[0].double())) * want.abs() + R.TINY[dt]
+    assert ((db - want).abs() <= bound).all(), ((db - want).abs() / bound).max()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_huge_arguments(D, act):
+    """Values and slopes where z^2 and z^3 pass the range of fp32: z and 1
+    above, 0 and 0 below."""
+    z = torch.tensor([1e19, 3e19, 1e25, 3e38, -1e19, -3e19, -1e25, -3e38], device="cuda").to(BF)
+    y, at = through_linear(D, z, act, 8)
+    assert torch.equal(y, torch.where(at > 0, at, 0 * at)[:, None].expand(8, 16))
+    one, w = torch.ones(1, 8, dtype=BF, device="cuda"), torch.zeros(8, 8, dtype=BF, device="cuda")
+    db = D.linear_backward(one, one, w, z[None], act, bias=True)[2]
+    assert torch.equal(db, (z > 0).to(BF))
+    # through the gated block: gate z, up 1, down 1
+    x, w13, w2 = torch.zeros(8, 8, dtype=BF, device="cuda"), torch.zeros(16, 8, dtype=BF, device="cuda"), torch.zeros(8, 8, dtype=BF, device="cuda")
+    x[:, 0], x[:, 1], w13[0, 0], w13[8, 1], w2[0, 0] = z, 1, 1, 1, 1
+    y, gu = D.gated_ffn(x, w13, w2, act, save=True)
+    assert torch.equal(y[:, 0], torch.where(z > 0, z, 0 * z))
+    dy = torch.zeros_like(x)
+    dy[:, 0] = 1
+    dx = D.gated_ffn_backward(dy, x, w13, w2, gu, act)[0]
+    assert torch.equal(dx[:, 0], (z > 0).to(BF)) and torch.equal(dx[:, 1], torch.where(z > 0, z, 0 * z))
