@@ -75,7 +75,7 @@ def through_linear(D, z, act, rows, **kw):
     return D.linear(x, w, act=act, **kw), x[:, 0]
 
 
-TAILS = [("gelu_tanh", BF), ("gelu_tanh", HF)]
+TAILS = [(a, t) for a in TAIL for t in (BF, HF)]
 
 
 @pytest.mark.parametrize("act,dt", TAILS)
