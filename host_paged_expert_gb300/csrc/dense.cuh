@@ -254,7 +254,7 @@ constexpr float kGeluCubic = 0.044715f;
 __device__ __forceinline__ float gelu_gate(float z) { return sigmoid_f(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)); }
 
 // Phi(z), and e = e^(-z^2/2).  0.5 + 0.5 erf(z / sqrt 2) cancels at z < 0 (at z
-// = -5 a fifth of it is left), so the tail is computed as such: Phi(-y) = e t
+// = -5 a tenth of it is lost), so the tail is computed as such: Phi(-y) = e t
 // Q(t), t = 1 / (1 + 0.28 y), the form of Hastings' approximations (1955), with
 // Q fitted here: degree 8, the relative error of t Q(t) against
 // erfcx(y / sqrt 2) / 2 levelled over 0 < t <= 1 at 1.7e-7.  In fp32 within 5e-7,

@@ -54,7 +54,8 @@ constexpr PairCost kWide = {5.2, 0.1, 0.265, 0.5, 2.65, 0.11, 2.7}, kNarrow = {3
 double epi_extra(const Product& p, EpiKind kind, int tn) {
     if (kind == EPI_GATED) return tn == 128 ? 0.7 : 0.0;
     if (kind != EPI_LINEAR) return 0;
-    return (p.e.act != PE_ACT_NONE ? 0.8 : 0.0) + (p.e.bias ? 0.2 : 0.0) + (p.e.res ? 0.9 : 0.0) + (p.e.keep ? 0.5 : 0.0);
+    return (p.e.act != PE_ACT_NONE ? 0.8 : 0.0) + (p.e.bias ? 0.2 : 0.0) + (p.e.res ? 0.9 : 0.0) + (p.e.keep ? 0.5 : 0.0) +
+           (p.e.out_f32 ? 0.9 : 0.0);
 }
 
 double tile_time(const PairCost& c, int kb, double extra) {
@@ -111,13 +112,16 @@ Choice choose(const Product& p, EpiKind kind) {
     const bool fp8 = p.a_scale != nullptr, f32 = p.e.out_f32 != 0;
     const int kb = up(p.K, fp8 ? 128 : 64);
     Choice c;
-    // fp32 results of more than 8 blocks stay with the kernel that bounds the terms of one accumulator
-    if (!f32 || fp8 || kb <= 8)
+    bool bounded = !f32 || fp8;  // whether the best kernel keeps its accumulators to 8 blocks, where that matters
+    // fp32 results of more than 8 blocks stay with the kernel that bounds the terms of one accumulator, and
+    // so do those of ragged columns, stored one by one (cluster split / CTA pairs: 700 x 512 x 777 8.6 / 12.6
+    // us, 6508 x 344 x 310 15.8 / 17.0; with whole vectors 6508 x 344 x 304 11.1 / 8.5, 8192 x 512 x 512 14.1 /
+    // 9.9, 4096 x 512 x 32000 328 / 128)
+    if (!f32 || fp8 || (kb <= 8 && p.e.vec))
         for (int t = 256; t >= (fp8 ? 256 : 128); t /= 2) {
             const double us = pair_time(p, kind, t);
-            if (us < c.us) c.us = us, c.tn = t;
+            if (us < c.us) c.us = us, c.tn = t, bounded = true;
         }
-    bool bounded = !f32 || fp8;  // whether the best shape keeps its accumulators to 8 blocks, where that matters
     for (int most = 32; most <= (fp8 ? 64 : 128); most *= 2) {
         // rows shared out evenly over the fewest tiles of at most `most`
         SplitShape s;

@@ -117,3 +117,22 @@ def test_huge_arguments(D, act):
     dy[:, 0] = 1
     dx = D.gated_ffn_backward(dy, x, w13, w2, gu, act)[0]
     assert torch.equal(dx[:, 0], (z > 0).to(BF)) and torch.equal(dx[:, 1], torch.where(z > 0, z, 0 * z))
+
+
+# ---- fp32 results
+
+
+@pytest.mark.parametrize("rows,k,n", [(5000, 512, 520), (6508, 344, 310), (3001, 72, 1000), (2500, 8, 2047), (4096, 512, 4096)])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("full", [False, True])
+def test_fp32_results_of_many_rows(D, rows, k, n, dt, full):
+    """K of up to 512 and many rows: the kernel of CTA pairs, whole and ragged
+    columns."""
+    x, w = rand(rows, k, dt=dt), rand(n, k, seed=1, scale=k**-0.5, dt=dt)
+    b, res, act = (rand(n, seed=2, dt=dt), rand(rows, n, seed=3, dt=dt), "silu") if full else (None, None, "none")
+    y, z = D.linear(x, w, b, act, res, out_dtype=F32, save=True)
+    want = R.linear(x, w, b, act, res, dt, F32)
+    R.check(y, want["y"], "fp32")
+    if full:
+        R.check(z, want["z"], "z")
+    assert same(D.linear(x, w, b, act, res, out_dtype=F32), y)
