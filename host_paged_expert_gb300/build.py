@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -46,24 +47,33 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile and link libpe.so; returns its path."""
+    """Compile and link libpe.so, then the Python binding; returns the
+    library's path.  The library needs nvcc alone and is in place before the
+    binding is asked for; a host without torch gets no binding."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = list(extra or [])
     if verbose:
         extra += ["-Xptxas", "-v"]
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)  # the longest one first
+        # the longest one first
+        binding = ex.submit(_compile_binding) if importlib.util.find_spec("torch") else None
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        binding = binding.result()
+        _link(objs)
+    if binding is None:
+        print("torch is not installed: libpe.so is built, the Python binding of the dense operators is not", file=sys.stderr)
+    else:
+        _link_binding(binding.result())
+    return LIB
+
+
+def _link(objs: list[str]) -> None:
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
-    return LIB
 
 
 def _compile_binding() -> str:
