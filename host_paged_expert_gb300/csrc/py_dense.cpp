@@ -11,6 +11,7 @@
 #include <stdio.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -53,6 +54,10 @@ Ten load(PyObject* o, const char* name) {
     }
     const at::Tensor& t = THPVariable_Unpack(o);
     if (t.layout() != at::kStrided) bad(PE_ERR_INVALID, "%s: want a dense tensor", name);
+    // a result without a graph would drop the tensor's gradient without a word
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        bad(PE_ERR_INVALID, "%s requires grad, and these calls record none: detach it, or call under torch.no_grad() or inside a "
+                            "torch.autograd.Function", name);
     Ten r;
     r.there = true;
     r.dt = t.scalar_type();

@@ -8,7 +8,8 @@ read may have any row pitch that is a multiple of 16 bytes, everything else is
 contiguous.  Calls are asynchronous on the current stream, or on ``stream``;
 then results and workspaces belong to that stream.  Invalid arguments raise
 PEError.  There is no autograd: ``save=True`` returns what the backward call
-needs.
+needs, and a tensor that requires gradients is refused unless gradients are
+off (``torch.no_grad()``, or inside a ``torch.autograd.Function``).
 """
 
 from __future__ import annotations

@@ -91,3 +91,53 @@ def test_misaligned_scales(L, off):
     a[2], a[4] = A + off[0], A + off[1]
     assert L.pe_linear(*a) == _lib.PE_ERR_INVALID
     assert b"scales must be 4-byte aligned" in L.pe_last_error(None)
+
+
+# ---- tensors that require gradients
+
+
+def _grad_calls():
+    import torch
+
+    from host_paged_expert_gb300 import dense as D
+
+    t = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    x, n, w, w13, w2, rs, y = t(4, 64), t(64), t(24, 64), t(32, 64), t(64, 16), t(4, dt=torch.float32), t(4, 24)
+    return {
+        "rms_norm": (D.rms_norm, (x, n, x)),
+        "rms_norm_backward": (D.rms_norm_backward, (x, x, n, rs, x)),
+        "linear": (D.linear, (x, w, t(24), "none", y)),
+        "linear_backward": (D.linear_backward, (y, x, w, y, "silu")),
+        "gated_ffn": (D.gated_ffn, (x, w13, w2, "silu", x)),
+        "gated_ffn_backward": (D.gated_ffn_backward, (x, x, w13, w2, t(4, 32))),
+    }
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward"])
+def test_gradients_are_not_dropped_without_a_word(name):
+    torch = pytest.importorskip("torch")
+    fn, args = _grad_calls()[name]
+    for i, a in enumerate(args):
+        if not isinstance(a, torch.Tensor):
+            continue
+        these = list(args)
+        these[i] = a.clone().requires_grad_()
+        with pytest.raises(_lib.PEError, match="requires grad") as e:
+            fn(*these)
+        assert e.value.status == _lib.PE_ERR_INVALID
+        with torch.no_grad(), pytest.raises(_lib.PEError, match="want CUDA tensors"):
+            fn(*these)
+
+
+def test_inside_an_autograd_function():
+    torch = pytest.importorskip("torch")
+    from host_paged_expert_gb300 import dense
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            return dense.linear(x, w)
+
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(24, 64, dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(_lib.PEError, match="want CUDA tensors"):  # nothing else is wrong with it
+        Linear.apply(x, w)
