@@ -6,7 +6,9 @@ Tensors are torch CUDA tensors of one device: bf16 or fp16 (``linear`` also
 takes E4M3 with scales).  Matrices are [rows, features]; activations that are
 read may have any row pitch that is a multiple of 16 bytes, everything else is
 contiguous.  Calls are asynchronous on the current stream, or on ``stream``;
-then results and workspaces belong to that stream.  Invalid arguments raise
+then results and workspaces belong to that stream, which has to wait for what
+made the arguments, and the arguments may be freed as soon as the call returns.
+Invalid arguments raise
 PEError.  There is no autograd: ``save=True`` returns what the backward call
 needs, and a tensor that requires gradients is refused unless gradients are
 off (``torch.no_grad()``, or inside a ``torch.autograd.Function``).
@@ -51,7 +53,11 @@ def _elsewhere(call, dev: int, stream, args):
     if stream.device.index != dev:
         _raise(1, f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     with torch.cuda.stream(stream):  # makes the stream's device current
-        return call(*args, None)
+        out = call(*args, None)
+    for a in args:  # their memory stays theirs until the stream is past the call
+        if isinstance(a, torch.Tensor):
+            a.record_stream(stream)
+    return out
 
 
 _native = None

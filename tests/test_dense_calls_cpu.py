@@ -141,3 +141,29 @@ def test_inside_an_autograd_function():
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(24, 64, dtype=torch.bfloat16, requires_grad=True)
     with pytest.raises(_lib.PEError, match="want CUDA tensors"):  # nothing else is wrong with it
         Linear.apply(x, w)
+
+
+# ---- another stream
+
+
+def test_arguments_outlive_the_call_on_another_stream(monkeypatch):
+    """The allocator hears of the stream that a call's tensors are used on."""
+    import contextlib
+
+    torch = pytest.importorskip("torch")
+    from host_paged_expert_gb300 import dense
+
+    seen = []
+
+    class T(torch.Tensor):
+        def record_stream(self, stream):
+            seen.append((self.data_ptr(), stream))
+
+    class Stream:
+        device = torch.device("cuda:0")
+
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    x, w = torch.zeros(4, 64).as_subclass(T), torch.zeros(24, 64).as_subclass(T)
+    s = Stream()
+    assert dense._elsewhere(lambda *a: a, 0, s, (x, w, None, "none", None)) == (x, w, None, "none", None, None)
+    assert seen == [(x.data_ptr(), s), (w.data_ptr(), s)]

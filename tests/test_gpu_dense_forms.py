@@ -136,3 +136,25 @@ def test_fp32_results_of_many_rows(D, rows, k, n, dt, full):
     if full:
         R.check(z, want["z"], "z")
     assert same(D.linear(x, w, b, act, res, out_dtype=F32), y)
+
+
+# ---- another stream
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_arguments_freed_behind_a_call_on_another_stream(D, rows):
+    """Temporaries of a call on a busy stream, freed and their memory asked for
+    again before the call's kernels have run."""
+    x, w, w13, w2 = rand(rows, 256), rand(136, 256, seed=1), rand(144, 256, seed=2), rand(256, 72, seed=3)
+    want = [D.linear(x, w), D.gated_ffn(x, w13, w2, residual=x), D.rms_norm(x, w[0].contiguous(), x).y]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a, b, c = x.clone(), x.clone(), x.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # some ms
+    got = [D.linear(a, w, stream=s), D.gated_ffn(b, w13, w2, residual=b, stream=s), D.rms_norm(c, w[0].contiguous(), c, stream=s).y]
+    del a, b, c
+    over = [torch.full_like(x, float("nan")) for _ in range(8)]
+    s.synchronize()
+    assert len(over) == 8 and all(same(g, h) for g, h in zip(got, want))
