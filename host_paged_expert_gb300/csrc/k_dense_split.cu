@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool ok = true;
         int s = 0, buf = 0, in_buf = 0;
         uint32_t phase = 0, buf_phase = 1;
+        pdl_wait();  // a wait's limit is for this kernel's own copies, not for the launch before it
         for (int i = 0; i < nkb; ++i) {
             // FP8: each stage has the next buffer to itself; else a buffer takes sub_len stages
             if (FP8 && !(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err))) break;

@@ -77,3 +77,12 @@ def test_pair_kernel_stays_until_the_last_arrivals():
     issuer = rest[: rest.index("} else {\n")]
     assert producer.rindex("mbar_spin(&S.empty[s]") > producer.rindex("tma_load_2d_pair(")
     assert issuer.rindex("mbar_spin(&S.acc_empty[buf]") > issuer.rindex("mma_commit_pair(&S.acc_full[buf])")
+
+
+def test_split_kernel_waits_for_its_own_copies_only():
+    """A wait that counts its polls starts once the launch before is done:
+    however long that one takes, it uses up no limit."""
+    text = code("k_dense_split.cu")
+    issuer, rest = text[text.index("} else if (warp == 1) {") :].split("} else if (warp >= 4) {", 1)
+    for part in (issuer, rest[: rest.index("__syncthreads();")]):
+        assert "pdl_wait();" in part and part.index("pdl_wait();") < part.index("mbar_spin(")
