@@ -33,7 +33,7 @@ EXPORTS = [
     "pe_destroy", "pe_last_error", "pe_expert_mlp_noalloc", "pe_selftest_bounded_waits",
     "pe_rms_norm", "pe_rms_norm_backward", "pe_rms_norm_backward_workspace", "pe_linear", "pe_linear_backward",
     "pe_linear_backward_workspace", "pe_gated_ffn", "pe_gated_ffn_workspace", "pe_gated_ffn_backward",
-    "pe_gated_ffn_backward_workspace", "pe_dense_error",
+    "pe_gated_ffn_backward_workspace", "pe_dense_error", "pe_selftest_dense_waits",
 ]
 
 
@@ -118,6 +118,7 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).argtypes = args
         getattr(L, name).restype = c_size_t
     L.pe_dense_error.argtypes = [POINTER(c_uint32)]
+    L.pe_selftest_dense_waits.argtypes = [c_uint32, P, N, POINTER(c_uint32)]
     L.pe_last_error.argtypes = [c_void_p]
     L.pe_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:

@@ -88,11 +88,23 @@ cudaError_t launch_products(const Product* p, int count, int elem, uint32_t* err
 struct SplitShape {
     int nt, split;
 };
+// Polls after which a wait inside one of these kernels gives up.  A poll
+// suspends the thread for up to a microsecond or so by itself, so this is
+// seconds.
+constexpr uint32_t kPolls = 1u << 22;
+// Other limits, by the role that waits (the producer of copies, the issuer of
+// MMAs, the warps that read the sums), for the self-test of the waits.  Its
+// kernels are instances of their own: a limit that is no constant takes up to
+// 0.4 us of a product (512 x 2048 to 2048 9.9 -> 10.4 us).
+struct WaitLimits {
+    uint32_t copies, mma, sums;
+};
 // launch_pairs: up to kMostProducts EPI_LINEAR products of 16-bit operands in one launch, else one.
 constexpr int kMostProducts = 3;
-cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st);
+cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st,
+                         const WaitLimits* limits = nullptr);
 cudaError_t launch_split(const Product& p, EpiKind kind, int elem, const SplitShape& s, int chain, uint32_t* err,
-                         cudaStream_t st);
+                         cudaStream_t st, const WaitLimits* limits = nullptr);
 // Up to kGemvRows rows, forward products: weights streamed by warps, no tensor core.
 constexpr int kGemvRows = 4;
 cudaError_t launch_gemv(const Product& p, EpiKind kind, int elem, int chain, cudaStream_t st);

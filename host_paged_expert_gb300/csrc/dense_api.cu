@@ -85,6 +85,34 @@ extern "C" pe_status pe_dense_error(uint32_t* word) {
     return done(e);
 }
 
+extern "C" pe_status pe_selftest_dense_waits(uint32_t poll_limit, void* scratch, size_t scratch_bytes, uint32_t* out12) {
+    if (!out12 || !scratch || poll_limit == 0) return bad("pe_selftest_dense_waits: NULL pointer or no polls");
+    if (scratch_bytes < PE_SELFTEST_DENSE_BYTES || !aligned(scratch, 256))
+        return bad("pe_selftest_dense_waits: scratch too small or not 256-byte aligned");
+    // operands and scales are zeros; a word of its own for each run
+    constexpr int M = 256, KB = 16, kOperands = M * KB * 128;
+    uint8_t* base = static_cast<uint8_t*>(scratch);
+    uint32_t* words = reinterpret_cast<uint32_t*>(base);
+    uint8_t *ab = base + 256, *out = ab + kOperands;
+    static_assert(256 + kOperands + 2 * M * M <= PE_SELFTEST_DENSE_BYTES, "the scratch holds operands and result");
+    cudaError_t e = cudaMemset(scratch, 0, PE_SELFTEST_DENSE_BYTES);
+    // one role gives up at once, the others after poll_limit polls
+    const WaitLimits gives_up[3] = {{poll_limit, 0, poll_limit}, {poll_limit, poll_limit, 0}, {0, poll_limit, poll_limit}};
+    for (int i = 0; !e && i < 12; ++i) {
+        const bool fp8 = i / 6 != 0, split = i / 3 % 2 != 0;
+        const int k = KB * (fp8 ? 128 : 64), m = split ? 64 : M, n = split ? 128 : M;
+        Product p = make(ab, k, 0, ab, k, 0, m, n, k);
+        if (fp8) p.a_scale = p.b_scale = reinterpret_cast<const float*>(ab);
+        p.e.out = out;
+        p.e.ld_out = n;
+        e = split ? launch_split(p, EPI_LINEAR, PE_ELEM_BF16, {64, 2}, CHAIN_NONE, words + i, 0, &gives_up[i % 3])
+                  : launch_pairs(&p, 1, EPI_LINEAR, PE_ELEM_BF16, 256, words + i, 0, &gives_up[i % 3]);
+    }
+    if (!e) e = cudaDeviceSynchronize();
+    if (!e) e = cudaMemcpy(out12, words, 12 * sizeof(uint32_t), cudaMemcpyDeviceToHost);
+    return done(e);
+}
+
 extern "C" pe_status pe_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                                  const void* weight, float eps, void* y, void* sum, void* codes, float* scales,
                                  float* rstd, int32_t rows, int32_t hidden, int32_t elem, void* stream) {

@@ -41,13 +41,24 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// Waits for a barrier phase without sleeping in between; bounded (a poll
-// suspends the thread for up to a microsecond or so by itself).
-__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, uint32_t* err) {
-    for (uint32_t i = 0; i < (1u << 22); ++i)
+// A warp waits for a barrier phase without sleeping in between, `limit` polls
+// at most.  Its lanes poll one address by one instruction, so that they pass or
+// give up together (a vote on it, after each wait, took 0.03 us a K block).
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     atomicOr(err, (uint32_t)PE_DEVERR_TIMEOUT);
     return false;
+}
+
+// Polls of a wait before a block ends for what is on its way into it, some
+// milliseconds.
+constexpr uint32_t kLeavePolls = 1u << 16;
+// After a wait gave up: about a millisecond for copies that no barrier here
+// tells of.
+__device__ __forceinline__ void settle() {
+    const long long t0 = clock64();
+    for (int i = 0; i < 1 << 16 && clock64() - t0 < 2000000; ++i) __nanosleep(256);
 }
 
 // One lane of a converged warp.  The loops that feed the tensor core are run
@@ -112,6 +123,11 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
             smem_u32(bar)),
         "h"((uint16_t)3)
         : "memory");
+}
+
+// The same, on this CTA's `bar` alone.
+__device__ __forceinline__ void mma_commit_pair_here(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Shared-memory descriptor of an operand tile written by TMA with 128-byte

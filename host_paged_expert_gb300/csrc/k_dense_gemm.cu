@@ -152,6 +152,7 @@ struct Work {
     int tiles[N];
     Divide across[N];  // by a product's tiles along its columns
     int count;
+    WaitLimits limit;
 };
 
 // A pair's way through them: tiles pair, pair + pairs, ...
@@ -175,14 +176,16 @@ struct Walk {
     }
 };
 
+// LIMITED: the waits' limits are the launch's.
 // NP: products that the launch may hold.  With one, its fields are constants
 // of the instructions; found by index they cost 5 % of a large product's time.
-template <typename E, int KIND, bool FP8, int TN, int NP>
+template <typename E, int KIND, bool FP8, int TN, int NP, bool LIMITED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, TN), 1)
     pair_kernel(const __grid_constant__ Work<NP> work, uint32_t* err) {
     constexpr int STAGES = stages(KIND, FP8, TN), kStage = stage_bytes(TN);
     constexpr int BK = FP8 ? 128 : 64;                      // elements of a 128-byte row
     constexpr int NT = KIND == EPI_GATED ? TN / 2 : TN;  // result columns of a tile
+    auto polls = [](uint32_t limit) { return LIMITED ? limit : kPolls; };
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -232,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                 const int m0 = mt * kTile + (int)rank * kHalf;
                 const int n0 = KIND == EPI_GATED ? (int)rank * p.e.cols + nt * NT : nt * NT + (int)rank * (TN / 2);
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!(ok = tc::mbar_spin(&S.empty[s], phase, err))) break;
+                    if (!(ok = tc::mbar_spin(&S.empty[s], phase, err, polls(work.limit.copies)))) break;
                     if (lead) {
                         if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * kStage);
                         const uint32_t bar = bar0 + 8 * s;
@@ -259,13 +262,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
             // The leader's MMAs arrive on this CTA's barriers: stay until the last of
             // them have (a stage never used passes at once).
             for (int i = 0; ok && i < STAGES; ++i) {
-                ok = tc::mbar_spin(&S.empty[s], phase, err);
+                ok = tc::mbar_spin(&S.empty[s], phase, err, polls(work.limit.copies));
                 if (++s == STAGES) s = 0, phase ^= 1;
             }
-            // after a wait gave up: let this pair's copies land before the block ends
-            if (!ok && rank == 0)
-                for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                    tc::mbar_wait(&S.full[i % STAGES], (i / STAGES) & 1, err, PE_DEVERR_TIMEOUT, 1u << 16);
+            // After a wait gave up: let the copies land before the block ends.  The
+            // leader's barriers tell of both CTAs' where both asked for a stage.
+            if (!ok) {
+                bool landed = rank == 0;
+                for (uint32_t i = issued > STAGES ? issued - STAGES : 0; landed && i < issued; ++i)
+                    landed = tc::mbar_wait(&S.full[i % STAGES], (i / STAGES) & 1, err, PE_DEVERR_TIMEOUT, tc::kLeavePolls);
+                if (!landed) tc::settle();
+            }
         } else if (warp == 1 && rank == 0) {
             // ---- MMA issuer
             const bool lead = tc::elect_one();
@@ -280,8 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                 const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), p.a_mn);
                 const uint64_t b0 = tc::operand_desc(tc::smem_u32(ring) + kOperand, p.b_mn);
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if ((FP8 || kb == 0) && !(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err))) break;
-                    if (!(ok = tc::mbar_spin(&S.full[s], phase, err))) break;
+                    if ((FP8 || kb == 0) && !(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, polls(work.limit.mma)))) break;
+                    if (!(ok = tc::mbar_spin(&S.full[s], phase, err, polls(work.limit.mma)))) break;
                     tc::fence_after_sync();
                     const bool last = FP8 || kb == kblocks - 1;
                     if (lead) {
@@ -302,13 +309,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
             }
             // the other CTA's epilogue warps arrive here too: stay until the last of them have
             for (int i = 0; ok && i < 2; ++i) {
-                ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err);
+                ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, polls(work.limit.mma));
                 buf ^= 1;
                 if (buf == 0) buf_phase ^= 1;
             }
             if (!ok) {  // the MMAs already issued read shared memory and write TMEM
-                if (lead) tc::mma_commit_pair(&S.drain);
-                tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, 1u << 16);
+                if (lead) tc::mma_commit_pair_here(&S.drain);
+                tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, tc::kLeavePolls);
             }
         }
     } else {
@@ -347,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                     const uint64_t sc = tc::pack2(__float_as_uint(next), __float_as_uint(next));
                     if (kb + 1 < kblocks && live) next = as[kb + 1] * bs[kb + 1];
                     const uint32_t buf = use_acc & 1, at = lanes + buf * TN + half * 128;
-                    if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
+                    if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, polls(work.limit.sums)))) break;
                     tc::fence_after_sync();
                     ++use_acc;
 #pragma unroll
@@ -387,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
                 constexpr int SHARE = epi_warps(KIND, FP8, TN) / 4;  // warps that share a tile's columns
                 Ahead<E, KIND> x;
                 x.load(p.e, lane, row0, nt * NT + half * (NT / SHARE));
-                if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err))) break;
+                if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, polls(work.limit.sums)))) break;
                 ++use_acc;
                 tc::fence_after_sync();
                 constexpr int CH = NT / SHARE / 32;  // 32-column chunks of this warp's share
@@ -429,14 +436,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(KIND, FP8, T
 }
 
 // Pairs that the device holds at once, looked up once per kernel.
-template <typename E, int KIND, bool FP8, int TN, int NP>
+template <typename E, int KIND, bool FP8, int TN, int NP, bool LIMITED>
 cudaError_t resident_pairs(int* out) {
     static std::atomic<int> known[64];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     int n = dev < 64 ? known[dev].load() : 0;
     if (!n) {
-        auto k = pair_kernel<E, KIND, FP8, TN, NP>;
+        auto k = pair_kernel<E, KIND, FP8, TN, NP, LIMITED>;
         if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(KIND, FP8, TN))) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
@@ -450,11 +457,12 @@ cudaError_t resident_pairs(int* out) {
     return cudaSuccess;
 }
 
-template <typename E, int KIND, bool FP8, int TN, int NP = 1>
-cudaError_t launch(const Product* p, int count, uint32_t* err, cudaStream_t st) {
+template <typename E, int KIND, bool FP8, int TN, int NP = 1, bool LIMITED = false>
+cudaError_t launch(const Product* p, int count, uint32_t* err, cudaStream_t st, const WaitLimits& limits = {}) {
     if (count < 1 || count > NP) return cudaErrorInvalidValue;
     Work<NP> w;
     w.count = count;
+    w.limit = limits;
     long long tiles = 0;
     for (int i = 0; i < count; ++i) {
         if (!encode_operand(&w.a[i], p[i].a, p[i].lda, p[i].M, p[i].K, p[i].a_mn, FP8, kHalf) ||
@@ -468,9 +476,9 @@ cudaError_t launch(const Product* p, int count, uint32_t* err, cudaStream_t st) 
         w.across[i] = Divide::by((p[i].e.cols + NT - 1) / NT);
     }
     int pairs = 0;
-    if (cudaError_t e = resident_pairs<E, KIND, FP8, TN, NP>(&pairs)) return e;
+    if (cudaError_t e = resident_pairs<E, KIND, FP8, TN, NP, LIMITED>(&pairs)) return e;
     if (tiles < pairs) pairs = (int)tiles;
-    return launch_pdl(pair_kernel<E, KIND, FP8, TN, NP>, dim3(2 * pairs), dim3(threads(KIND, FP8, TN)), smem_bytes(KIND, FP8, TN), st, w, err);
+    return launch_pdl(pair_kernel<E, KIND, FP8, TN, NP, LIMITED>, dim3(2 * pairs), dim3(threads(KIND, FP8, TN)), smem_bytes(KIND, FP8, TN), st, w, err);
 }
 
 template <typename E>
@@ -518,7 +526,11 @@ bool encode_operand(CUtensorMap* m, const void* base, int64_t ld, int rows, int 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st) {
+cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st,
+                         const WaitLimits* limits) {
+    if (limits)
+        return p->a_scale ? launch<__nv_bfloat16, EPI_LINEAR, true, 256, 1, true>(p, count, err, st, *limits)
+                          : launch<__nv_bfloat16, EPI_LINEAR, false, 256, 1, true>(p, count, err, st, *limits);
     return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, count, kind, tn, err, st)
                                 : launch_kind<__half>(p, count, kind, tn, err, st);
 }

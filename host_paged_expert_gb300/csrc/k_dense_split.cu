@@ -51,6 +51,7 @@ struct Plan {
     int sub_len;  // stages that one of them takes (16-bit operands)
     int cols;     // TMEM columns
     int early;    // load weights before the previous kernel is done
+    WaitLimits limit;
 };
 
 struct Shared {
@@ -121,12 +122,14 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
     }
 }
 
-template <typename E, int KIND, bool FP8>
+// LIMITED: the waits' limits are the launch's.
+template <typename E, int KIND, bool FP8, bool LIMITED>
 __global__ void __launch_bounds__(kThreads, 2)
     split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constant__ CUtensorMap tq,
                  const __grid_constant__ Product p, const __grid_constant__ Plan q, uint32_t* err) {
     constexpr int BK = FP8 ? 128 : 64;                            // elements of a 128-byte row
     constexpr int NF = KIND == EPI_GATED ? kRows / 2 : kRows;  // result columns of a tile
+    auto polls = [](uint32_t limit) { return LIMITED ? limit : kPolls; };
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -200,7 +203,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 0) {
         // ---- producer
         const bool lead = tc::elect_one();
-        bool ok = true;
         if (q.early) {
             pdl_wait();
             if (lead)
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         int i = pre, s = 0;
         uint32_t phase = 0;
         for (; i < nkb; ++i) {
-            if (!(ok = tc::mbar_spin(&S.empty[s], phase, err))) break;
+            if (!tc::mbar_spin(&S.empty[s], phase, err, polls(q.limit.copies))) break;
             if (lead) {
                 tc::mbar_arrive_expect_tx(&S.full[s], stage);
                 load_p(i, s);
@@ -217,10 +219,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             if (++s == q.stages) s = 0, phase ^= 1;
         }
-        // after a wait gave up: let the copies land before the block ends
-        if (!ok)
-            for (int j = max(0, i - q.stages); j < i; ++j)
-                tc::mbar_wait(&S.full[j % q.stages], (j / q.stages) & 1, err, PE_DEVERR_TIMEOUT, 1u << 16);
+        // the block does not end before its copies have landed (all of them were used, unless a wait gave up)
+        bool landed = true;
+        for (int j = max(0, i - q.stages); landed && j < i; ++j)
+            landed = tc::mbar_wait(&S.full[j % q.stages], (j / q.stages) & 1, err, PE_DEVERR_TIMEOUT, tc::kLeavePolls);
+        if (!landed) tc::settle();
     } else if (warp == 1) {
         // ---- MMA issuer
         const bool lead = tc::elect_one();
@@ -228,14 +231,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t id = tc::idesc(FMT, p.b_mn, p.a_mn, kRows, q.nt);
         const uint32_t pstep = (p.b_mn ? 2048 : 32) >> 4, qstep = (p.a_mn ? 2048 : 32) >> 4;
         const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), p.b_mn), b0 = tc::operand_desc(tc::smem_u32(ring) + kP, p.a_mn);
-        bool ok = true;
         int s = 0, buf = 0, in_buf = 0;
         uint32_t phase = 0, buf_phase = 1;
         pdl_wait();  // a wait's limit is for this kernel's own copies, not for the launch before it
         for (int i = 0; i < nkb; ++i) {
             // FP8: each stage has the next buffer to itself; else a buffer takes sub_len stages
-            if (FP8 && !(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err))) break;
-            if (!(ok = tc::mbar_spin(&S.full[s], phase, err))) break;
+            if (FP8 && !tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, polls(q.limit.mma))) break;
+            if (!tc::mbar_spin(&S.full[s], phase, err, polls(q.limit.mma))) break;
             tc::fence_after_sync();
             if (lead) {
                 const uint64_t a = a0 + (uint32_t)(s * stage >> 4), b = b0 + (uint32_t)(s * stage >> 4);
@@ -253,10 +255,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (++buf == q.subs) buf = 0, buf_phase ^= 1;
             }
         }
-        if (!ok) {  // the MMAs already issued read shared memory and write TMEM
-            if (lead) tc::mma_commit(&S.drain);
-            tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, 1u << 16);
-        }
+        // nor before its MMAs, which read shared memory and write TMEM
+        if (lead) tc::mma_commit(&S.drain);
+        tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, tc::kLeavePolls);
     } else if (warp >= 4) {
         // ---- accumulators to part[token][weight row]
         pdl_wait();
@@ -270,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
             const float* bs = p.b_scale + (size_t)ft * kall + kb0;
-            bool ok = true;
             int buf = 0;
             uint32_t phase = 0;
             for (int i = 0; i < nkb; ++i) {
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int t = t0 + c * 32 + lane;
                     xs[c] = t < p.M && c * 32 + lane < q.nt ? ws * p.a_scale[(size_t)t * kall + kb0 + i] : 0.f;
                 }
-                if (!(ok = tc::mbar_spin(&S.acc_full[buf], phase, err))) break;
+                if (!tc::mbar_spin(&S.acc_full[buf], phase, err, polls(q.limit.sums))) break;
                 tc::fence_after_sync();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int j = 0; j < 32; ++j)
                     if (c * 32 + j < q.nt) part[(c * 32 + j) * kRows] = acc[c][j];
         } else {
-            if (tc::mbar_spin(&S.acc_full[0], 0, err)) {
+            if (tc::mbar_spin(&S.acc_full[0], 0, err, polls(q.limit.sums))) {
                 tc::fence_after_sync();
                 // the next chunk is on its way while this one is stored; two arrays in turn
                 uint32_t r[2][32];
@@ -377,12 +377,13 @@ int sub_count(const SplitShape& s, int kb) {
     return want < most ? want : most;
 }
 
-template <typename E, int KIND, bool FP8>
-cudaError_t launch(const Product& p, const SplitShape& s, int chain, uint32_t* err, cudaStream_t st) {
+template <typename E, int KIND, bool FP8, bool LIMITED = false>
+cudaError_t launch(const Product& p, const SplitShape& s, int chain, uint32_t* err, cudaStream_t st,
+                   const WaitLimits& limits = {}) {
     static std::atomic<uint64_t> ready;  // devices whose attribute is set
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    auto kernel = split_kernel<E, KIND, FP8>;
+    auto kernel = split_kernel<E, KIND, FP8, LIMITED>;
     if (dev >= 64 || !(ready.load() >> dev & 1)) {
         if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) return e;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
@@ -410,6 +411,7 @@ cudaError_t launch(const Product& p, const SplitShape& s, int chain, uint32_t* e
     const long long blocks = (long long)q.ftiles * ((p.M + s.nt - 1) / s.nt) * s.split;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
     q.early = chain == CHAIN_AFTER;
+    q.limit = limits;
     CUtensorMap tp, tq;
     if (!encode_operand(&tp, p.b, p.ldb, p.N, p.K, p.b_mn, FP8, 64) || !encode_operand(&tq, p.a, p.lda, p.M, p.K, p.a_mn, FP8, s.nt))
         return cudaErrorInvalidValue;
@@ -458,7 +460,7 @@ int split_resident(const SplitShape& s) {
     cfg.dynamicSmemBytes = block_bytes(s.nt);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto k = split_kernel<__nv_bfloat16, EPI_LINEAR, false>;
+    auto k = split_kernel<__nv_bfloat16, EPI_LINEAR, false, false>;
     int c = 0;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess &&
         cudaOccupancyMaxActiveClusters(&c, k, &cfg) == cudaSuccess && c > 0)
@@ -472,7 +474,10 @@ int split_resident(const SplitShape& s) {
 }
 
 cudaError_t launch_split(const Product& p, EpiKind kind, int elem, const SplitShape& s, int chain, uint32_t* err,
-                         cudaStream_t st) {
+                         cudaStream_t st, const WaitLimits* limits) {
+    if (limits)
+        return p.a_scale ? launch<__nv_bfloat16, EPI_LINEAR, true, true>(p, s, chain, err, st, *limits)
+                         : launch<__nv_bfloat16, EPI_LINEAR, false, true>(p, s, chain, err, st, *limits);
     return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, s, chain, err, st)
                                 : launch_kind<__half>(p, kind, s, chain, err, st);
 }

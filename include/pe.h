@@ -470,6 +470,20 @@ pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, const void* x
  * device. */
 pe_status pe_dense_error(uint32_t* word);
 
+/* Self-test of the waits inside the dense operators' kernels, as
+ * pe_selftest_bounded_waits (which see): a product of the pair kernel and one
+ * of the split kernel, of 16-bit and of E4M3 operands, in which one role gives
+ * up at once and the others, waiting for it, after `poll_limit` polls.
+ *   out12[6 e + 3 k + r]: the error word with operands e (0 bf16, 1 E4M3), kernel
+ *     k (0 pairs, 1 split) and role r (0 the issuer of MMAs, with copies on
+ *     their way; 1 the warps that read the sums, with MMAs running; 2 the
+ *     producer of copies).
+ * Each word must read PE_DEVERR_TIMEOUT; pe_dense_error is not touched.
+ * scratch: PE_SELFTEST_DENSE_BYTES of device memory, 256-byte aligned.
+ * Synchronises the device. */
+#define PE_SELFTEST_DENSE_BYTES (1u << 20)
+pe_status pe_selftest_dense_waits(uint32_t poll_limit, void* scratch, size_t scratch_bytes, uint32_t* out12);
+
 /* Frees the host store (if owned) and the handle; never the arena. */
 void pe_destroy(pe_handle* h);
 

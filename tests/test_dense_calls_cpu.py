@@ -167,3 +167,12 @@ def test_arguments_outlive_the_call_on_another_stream(monkeypatch):
     s = Stream()
     assert dense._elsewhere(lambda *a: a, 0, s, (x, w, None, "none", None)) == (x, w, None, "none", None, None)
     assert seen == [(x.data_ptr(), s), (w.data_ptr(), s)]
+
+
+def test_selftest_of_the_waits_refuses(L):
+    import ctypes
+
+    out = (ctypes.c_uint32 * 12)()
+    call = L.pe_selftest_dense_waits
+    assert [call(0, A, 1 << 20, out), call(9, None, 1 << 20, out), call(9, A, (1 << 20) - 1, out), call(9, A + 16, 1 << 20, out),
+            call(9, A, 1 << 20, None)] == [_lib.PE_ERR_INVALID] * 5

@@ -158,3 +158,19 @@ def test_arguments_freed_behind_a_call_on_another_stream(D, rows):
     over = [torch.full_like(x, float("nan")) for _ in range(8)]
     s.synchronize()
     assert len(over) == 8 and all(same(g, h) for g, h in zip(got, want))
+
+
+# ---- waits that run out
+
+
+def test_waits_give_up_and_report(D):
+    """Each role of the tensor-core kernels in turn gives up at once, the
+    others when their polls run out: the words say so, nothing hangs, and what
+    runs next is as it was."""
+    x, w, w13, w2 = rand(300, 2048), rand(2048, 2048, seed=1, scale=0.02), rand(512, 2048, seed=2, scale=0.02), rand(2048, 256, seed=3, scale=0.06)
+    run = lambda: [D.linear(x, w), D.linear(x[:8], w), D.gated_ffn(x, w13, w2), D.linear(x.repeat(9, 1), w)]  # noqa: E731
+    want = run()
+    for polls in (1, 1 << 6, 1 << 12):
+        assert D.selftest_waits(polls) == [0x8] * 12  # PE_DEVERR_TIMEOUT
+    assert D.error_word() == 0
+    assert all(same(a, b) for a, b in zip(run(), want))
