@@ -16,11 +16,11 @@ MAIN = r"""
 #include <string.h>
 #include "dense_plan.cu"
 namespace pe { namespace dense {
-cudaError_t launch_pairs(const Product*, int count, EpiKind, int, int tn, uint32_t*, cudaStream_t) {
+cudaError_t launch_pairs(const Product*, int count, EpiKind, int, int tn, uint32_t*, cudaStream_t, const WaitLimits*) {
     printf("pairs %d %d\n", tn, count);
     return cudaSuccess;
 }
-cudaError_t launch_split(const Product&, EpiKind, int, const SplitShape& s, int, uint32_t*, cudaStream_t) {
+cudaError_t launch_split(const Product&, EpiKind, int, const SplitShape& s, int, uint32_t*, cudaStream_t, const WaitLimits*) {
     printf("split %d %d\n", s.nt, s.split);
     return cudaSuccess;
 }
