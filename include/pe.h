@@ -358,7 +358,11 @@ pe_status pe_expert_mlp_noalloc(const void* w13, const void* w2, const void* x, 
  *     once, when it is stored.
  *   - rows = 0 is a no-op, except that weight gradients are then set to zero;
  *     more than PE_MAX_ROWS are refused (PE_ERR_RANGE).
- *   - Results do not depend on timing: the same call gives the same bits.
+ *   - Ranges are those of the types: a 16-bit result or intermediate (h of the
+ *     gated block, dz, dg, du) beyond fp16's 65504 is infinite, and the
+ *     squares of a norm are summed in fp32 (rows of about 1e19 give 0).
+ *   - Results do not depend on timing: the same call gives the same bits (one
+ *     that leaves results out may take another kernel and order of its sums).
  *   - Errors: PE_ERR_INVALID (NULL, misaligned, bad sizes or types),
  *     PE_ERR_RANGE (above a stated limit), PE_ERR_CUDA; the message is in
  *     pe_last_error(NULL). */

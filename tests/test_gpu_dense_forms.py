@@ -2,6 +2,7 @@
 go wrong without a test of whole matrices seeing it."""
 
 import math
+import threading
 
 import pytest
 
@@ -174,3 +175,173 @@ def test_waits_give_up_and_report(D):
         assert D.selftest_waits(polls) == [0x8] * 12  # PE_DEVERR_TIMEOUT
     assert D.error_word() == 0
     assert all(same(a, b) for a, b in zip(run(), want))
+
+
+# ---- every activation's backward pass
+
+
+@pytest.mark.parametrize("rows,k,n", [(5, 64, 72), (131, 264, 77), (700, 520, 264)])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_backward_of_each_activation(D, rows, k, n, dt, act):
+    x, w, dy = rand(rows, k, dt=dt), rand(n, k, seed=1, scale=2 * k**-0.5, dt=dt), rand(rows, n, seed=3, dt=dt)
+    _, z = D.linear(x, w, act=act, save=True)
+    want = R.linear_backward(dy, x, w, z, act, dt)
+    for g, name in zip(D.linear_backward(dy, x, w, z, act, bias=True), ("dx", "dw", "db")):
+        R.check(g, want[name], name)
+
+
+@pytest.mark.parametrize("rows,h,i", [(3, 64, 72), (131, 264, 200), (1100, 136, 520)])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_ffn_backward_of_each_activation(D, rows, h, i, dt, act):
+    x, w13, w2 = rand(rows, h, dt=dt), rand(2 * i, h, seed=1, scale=2 * h**-0.5, dt=dt), rand(h, i, seed=2, scale=i**-0.5, dt=dt)
+    dy = rand(rows, h, seed=4, dt=dt)
+    _, gu = D.gated_ffn(x, w13, w2, act, save=True)
+    want = R.gated_ffn_backward(dy, x, w13, w2, gu, act, dt)
+    for g, name in zip(D.gated_ffn_backward(dy, x, w13, w2, gu, act), ("dx", "dw13", "dw2")):
+        R.check(g, want[name], name)
+
+
+def test_gradients_that_are_not_wanted(D):
+    """The C calls with each gradient alone (which may take another kernel than
+    all of them together, so it is the formulas that they are held against)."""
+    from host_paged_expert_gb300 import _lib
+
+    L, st = _lib.lib(), torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    x, w, dy = rand(131, 264), rand(77, 264, seed=1, scale=0.06), rand(131, 77, seed=3)
+    _, z = D.linear(x, w, act="silu", save=True)
+    want = R.linear_backward(dy, x, w, z, "silu", BF)
+    for i, k in enumerate(("dx", "dw", "db")):
+        out = [None, None, None]
+        out[i] = torch.full_like(want[k].v, float("nan"), dtype=BF)
+        need = [x if i == 1 else None, w if i == 0 else None]
+        assert L.pe_linear_backward(p(dy), 77, p(need[0]), 264, p(need[1]), p(z), 1, *map(p, out), p(ws), ws.numel(), 131, 264, 77, 0, st) == 0
+        R.check(out[i], want[k], k)
+    h, i_ = 264, 200
+    w13, w2, dy = rand(2 * i_, h, seed=1, scale=0.06), rand(h, i_, seed=2, scale=0.06), rand(131, h, seed=4)
+    _, gu = D.gated_ffn(x, w13, w2, save=True)
+    want = R.gated_ffn_backward(dy, x, w13, w2, gu, "silu", BF)
+    for i, k in enumerate(("dx", "dw13", "dw2")):
+        out = [None, None, None]
+        out[i] = torch.full_like(want[k].v, float("nan"), dtype=BF)
+        assert L.pe_gated_ffn_backward(p(dy), h, p(x if i == 1 else None), h, p(w13 if i == 0 else None), p(w2), p(gu), 1, *map(p, out),
+                                       p(ws), ws.numel(), 131, h, i_, 0, st) == 0
+        R.check(out[i], want[k], k)
+    # a norm's results one by one
+    n, res = rand(264, seed=5), rand(131, 264, seed=6)
+    f = D.rms_norm(x, n, res, quant=True, save=True)
+    for k in ("y", "sum", "rstd"):
+        out = torch.full_like(getattr(f, k), float("nan"))
+        a = {k: p(out)}
+        assert L.pe_rms_norm(p(x), 264, p(res), 264, p(n), 1e-6, a.get("y"), a.get("sum"), None, None, a.get("rstd"), 131, 264, 0, st) == 0
+        assert same(out, getattr(f, k))
+
+
+# ---- the order of launches
+
+
+@pytest.mark.parametrize("rows", [1, 4, 16, 64, 300])
+def test_weights_rewritten_right_before(D, rows):
+    """gated_ffn behind a launch that has just written w2, by a copy and by a
+    product: its second kernel may ask for w2 while the first one runs, no
+    earlier."""
+    x, w13 = rand(rows, 512), rand(2048, 512, seed=1, scale=0.04)
+    a, b, old = rand(512, 512, seed=2, scale=0.05), rand(1024, 512, seed=3), rand(512, 1024, seed=4)
+    new = D.linear(a, b)
+    torch.cuda.synchronize()
+    want = D.gated_ffn(x, w13, new)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        w2 = old.clone()
+        torch.cuda.synchronize()
+        w2.copy_(new)
+        y = D.gated_ffn(x, w13, w2)
+        del w2
+        stale = torch.full_like(new, float("nan"))
+        del stale  # its memory is what the product below writes
+        z = D.gated_ffn(x, w13, D.linear(a, b))
+        assert same(y, want) and same(z, want)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 16, 64, 300, 2500])
+def test_chains_of_launches(D, rows):
+    """Each call reads what the one before it has just written, in a graph with
+    nothing between the launches: the bits of calls that wait for each other."""
+    h = 512
+    x, n, wq = rand(rows, h), rand(h, seed=1), rand(640, h, seed=2, scale=0.05)
+    w1, w2, w13, wd = rand(h, 640, seed=3, scale=0.05), rand(h, h, seed=4, scale=0.05), rand(768, h, seed=5, scale=0.05), rand(h, 384, seed=6, scale=0.05)
+    codes, cs = (wq / 0.5).to(torch.float8_e4m3fn), torch.full((5, 4), 0.5, device="cuda")
+    buf = x.clone()
+
+    def chain(wait):
+        out, v = [], buf
+        for _ in range(4):
+            for step in (
+                lambda v: D.rms_norm(v, n, v, quant=True),
+                lambda m: D.linear(m.codes, codes, x_scale=m.scale, w_scale=cs),
+                lambda q: D.linear(q, w1, act="gelu"),
+                lambda v: D.linear(v, w2, residual=v),
+                lambda v: D.gated_ffn(v, w13, wd, residual=v),
+                lambda v: D.rms_norm(v, n).y,
+            ):
+                v = step(v)
+                if wait:
+                    torch.cuda.synchronize()
+                out.append(v.codes if isinstance(v, tuple) else v)
+        return out
+
+    want = [t.clone() for t in chain(True)]
+    g = torch.cuda.CUDAGraph()
+    buf.zero_()
+    with torch.cuda.graph(g):
+        got = chain(False)
+    g.replay()
+    buf.copy_(x)
+    for _ in range(10):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want))
+
+
+def test_two_host_threads(D):
+    """Calls from two threads on streams of their own."""
+    x, w, w13, w2, n = rand(300, 512), rand(264, 512, seed=1, scale=0.05), rand(528, 512, seed=2, scale=0.05), rand(512, 264, seed=3, scale=0.05), rand(512, seed=4)
+
+    def calls(t):
+        y, z = D.linear(x[:t], w, act="silu", save=True)
+        return [y, D.gated_ffn(x[:t], w13, w2), D.rms_norm(x[:t], n, x[:t], quant=True).codes, *D.linear_backward(y, x[:t], w, z, "silu", bias=True)]
+
+    want = {t: calls(t) for t in (1, 300)}
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(2)
+
+    def work(t):
+        s = torch.cuda.Stream()
+        start.wait()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                got = calls(t)
+                s.synchronize()
+                if not all(same(a, b) for a, b in zip(got, want[t])):
+                    wrong.append(t)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in want]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_fp16_range(D):
+    """fp16's range, as documented: h above 65504 becomes infinite between the
+    products, in its own row only; bf16 holds it."""
+    for dt in (HF, BF):
+        x, w13, w2 = torch.zeros(8, 8, dtype=dt, device="cuda"), torch.zeros(16, 8, dtype=dt, device="cuda"), torch.zeros(8, 8, dtype=dt, device="cuda")
+        x[:, 0], w13[0, 0], w13[8, 0], w2[0, 0] = 1, 1, 1, 2.0**-10
+        x[3, 0] = 1024  # h = 2^20, y = 2^10
+        y = D.gated_ffn(x, w13, w2, "none")[:, 0].float().tolist()
+        assert y == [2.0**-10] * 3 + [math.inf if dt == HF else 1024.0] + [2.0**-10] * 4
