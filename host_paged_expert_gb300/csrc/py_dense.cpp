@@ -167,11 +167,20 @@ at::Tensor empty(int dev, Type dt, int64_t r, int64_t c = -1) {
 void* ptr(const at::Tensor& t) { return t.defined() && t.numel() ? t.data_ptr() : nullptr; }
 PyObject* wrap(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
 
+// The interpreter lock is let go for the C call, and held again before anything
+// that it throws goes on.
+struct NoGil {
+    PyThreadState* const saved = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(saved); }
+};
 template <typename F>
 void call(F&& f) {
     pe_status st;
-    Py_BEGIN_ALLOW_THREADS st = f();
-    Py_END_ALLOW_THREADS if (st) bad(st, "%s", pe_last_error(nullptr));
+    {
+        NoGil go;
+        st = f();
+    }
+    if (st) bad(st, "%s", pe_last_error(nullptr));
 }
 
 PyObject* tuple(std::initializer_list<const at::Tensor*> ts) {

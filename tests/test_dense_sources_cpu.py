@@ -86,3 +86,12 @@ def test_split_kernel_waits_for_its_own_copies_only():
     issuer, rest = text[text.index("} else if (warp == 1) {") :].split("} else if (warp >= 4) {", 1)
     for part in (issuer, rest[: rest.index("__syncthreads();")]):
         assert "pdl_wait();" in part and part.index("pdl_wait();") < part.index("mbar_spin(")
+
+
+def test_binding_holds_the_lock_again_before_an_exception_goes_on():
+    """What a call lets go it takes back by a destructor: the macros' block
+    would leave a C++ exception (of torch's stream lookup) without the lock that
+    its translation into a Python one needs."""
+    text = code("py_dense.cpp")
+    assert "Py_BEGIN_ALLOW_THREADS" not in text
+    assert re.search(r"~\w+\(\)\s*\{\s*PyEval_RestoreThread\(", text)
