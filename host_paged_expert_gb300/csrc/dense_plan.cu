@@ -33,7 +33,7 @@ namespace pe {
 namespace dense {
 namespace {
 
-constexpr double kSms = 152, kPairs = 76;
+constexpr double kPairs = 76;
 
 int up(long long a, long long b) { return (int)((a + b - 1) / b); }
 
