@@ -95,7 +95,7 @@ constexpr uint32_t kPolls = 1u << 22;
 // Other limits, by the role that waits (the producer of copies, the issuer of
 // MMAs, the warps that read the sums), for the self-test of the waits.  Its
 // kernels are instances of their own: a limit that is no constant takes up to
-// 0.4 us of a product (512 x 2048 to 2048 9.9 -> 10.4 us).
+// 0.4 us of a product (512 x 2048 to 2048 10.4 instead of 9.9 us).
 struct WaitLimits {
     uint32_t copies, mma, sums;
 };

@@ -18,12 +18,12 @@
 //   300 x 6144 x 2048                               21.5 (64, 2)  17.2 (64, 3)  24.1 (64, 4)
 //
 //   rows x K x cols   warps streaming weights        best cluster split
-//   1 x 4096 x 2048         2.7                       5.2
-//   1 x 8192 x 8192        19.8                      23.1
-//   2 x 4096 x 4096         6.0                       6.7
-//   4 x 2048 x 2048         3.9                       4.3
-//   4 x 4096 x 4096         9.7                       6.5
-//   4 x 8192 x 8192        40.4                      23.2
+//   1 x 4096 x 2048         2.9                       5.8
+//   1 x 8192 x 8192        20.1                      25.1
+//   2 x 4096 x 4096         6.6                       7.0
+//   4 x 2048 x 2048         4.2                       4.6
+//   4 x 4096 x 4096        10.1                       7.0
+//   4 x 8192 x 8192        42.2                      24.6
 #include <algorithm>
 #include <cmath>
 
@@ -48,9 +48,12 @@ struct PairCost {
 constexpr PairCost kWide = {5.2, 0.1, 0.265, 0.5, 2.65, 0.11, 2.7}, kNarrow = {3.15, 0.45, 0.205, 0.42, 1.25, 0.03, 1.0};
 
 // What a linear epilogue does besides converting and storing (8192 x 256 to
-// 8192, 27 tiles of 128 columns a pair: plain 39 us, gelu_tanh 61, bias and
-// residual 68, gelu_tanh with its input kept 73, all of it 101); narrow tiles
-// of gate and up have half the epilogue warps.
+// 8192, 27 tiles of 128 columns a pair: plain 40 us, gelu_tanh 57, bias and
+// residual 69, gelu_tanh with its input kept 68, all of it 97); narrow tiles
+// of gate and up have half the epilogue warps; an fp32 store costs what the
+// read of a residual does (4096 x 512 to 32000, 53 tiles a pair: 128 us).
+// EPI_GATED_BWD, which reads and stores the most, is not measured and counts
+// as a plain one.
 double epi_extra(const Product& p, EpiKind kind, int tn) {
     if (kind == EPI_GATED) return tn == 128 ? 0.7 : 0.0;
     if (kind != EPI_LINEAR) return 0;

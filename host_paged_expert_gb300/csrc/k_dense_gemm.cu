@@ -19,15 +19,16 @@
 // A launch may hold several products (dx and the weights' gradients of a
 // backward pass): their tiles are dealt out as one sequence.
 //
-// Bound by the tensor cores: bf16 8192^3 560 us (1960 TFLOP/s), 4096^3 77 us
+// Bound by the tensor cores: bf16 8192^3 566 us (1940 TFLOP/s), 4096^3 79 us
 // with the tensor pipe active 90 % of the cycles; 256 tiles fill 76 pairs'
 // four waves to 84 %.  Where K is short the epilogue shows, its instructions
 // and its waits for TMEM and the patch (issue slots 37 % busy): with eight
-// warps a 256 x 256 tile takes 2.9 us at K = 128, its K blocks 0.53.  So tiles of 256 x 128 columns, the choice
-// for short K and heavy epilogues, have sixteen epilogue warps (8192 x 256 to
-// 8192 39 us, with gelu_tanh 61, with bias, residual and kept values too 101;
-// eight: 53, 84, 148); in tiles of 256 columns their patches cost a stage
-// (4096^3 2 % slower), gate and up would need twice the patches.
+// warps a 256 x 256 tile takes 2.9 us at K = 128, its K blocks 0.53.  So tiles
+// of 256 x 128 columns, the choice for short K and heavy epilogues, have
+// sixteen epilogue warps (8192 x 256 to 8192 40 us, 53 with eight; with
+// gelu_tanh 57, with bias, residual and kept values too 97); in tiles of 256
+// columns their patches cost a stage (4096^3 2 % slower), gate and up would
+// need twice the patches.
 //
 // E4M3 operands: a stage is 128 deep, one scale group.  Each stage's product
 // goes to its own TMEM buffer and the epilogue warps add it, times the row's

@@ -10,8 +10,8 @@
 // is a fixed tree: lanes, then warps in order.
 //
 // Bound by HBM, or by a launch's latency where the weights sit in L2: 1 x 8192
-// to 8192 19.8 us (6800 GB/s), 1 x 4096 to 2048 2.9 us, gated feed-forward
-// 1 x 2048 x 768 4.7 us.  From two tokens on the multiply-adds count, and the
+// to 8192 20.1 us (6680 GB/s), 1 x 4096 to 2048 2.9 us (3.2 with bias and
+// residual), gated feed-forward 1 x 2048 x 768 4.5 us.  From two tokens on the multiply-adds count, and the
 // tensor cores take over where weights are many.
 //
 // The second product of a feed-forward block asks for its first pieces of the
@@ -26,9 +26,9 @@ namespace {
 
 constexpr int kWarps = 8, kAhead = 4;
 // Weight bytes up to which the next launch may move in early: it hides the
-// next one's start (1 x 4096 x 2048, 17 MB: 2.9 instead of 3.0 us), but its
-// waiting blocks slow a long stream (1 x 8192 x 8192, 134 MB: 21.5 us instead
-// of 18.8).
+// next one's start (gated feed-forward 1 x 2048 x 768, 9 MB: 4.6 instead of 4.7
+// us; 1 x 4096 x 2048, 17 MB: no gain), but its waiting blocks slow a long
+// stream (1 x 8192 x 8192, 134 MB: 22.0 us instead of 19.7).
 constexpr size_t kLetGo = 32u << 20;
 
 struct Plan {

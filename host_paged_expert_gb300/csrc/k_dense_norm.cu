@@ -3,7 +3,7 @@
 // are bound by HBM: each element is read and written once, in 16-byte
 // vectors, and held in registers in between.  Measured (a plain copy
 // moves 6786 GB/s): 16384 x 4096 with residual and 8-bit output
-// 97 us (6270 GB/s), 16384 x 4096 backward 91 us (5930 GB/s); a single row
+// 97 us (6270 GB/s), 16384 x 4096 backward 92 us (5800 GB/s); a single row
 // 1.6 us, a launch's latency.
 #include "dense.cuh"
 #include "pe_device.cuh"
@@ -257,8 +257,10 @@ __global__ void __launch_bounds__(kMostThreads, NV == 1 ? 2 : 1) rms_norm_bwd_ke
 // fit: the row is held as it was read, the block's share of the weight's
 // gradient lies in shared memory (each thread its own columns, so that no
 // barrier is needed), and each vector of the next row is asked for as soon as
-// this row's is used up.  2048 x 32768: 128 us, 4180 GB/s (402 us with the
-// fp32 values in 128 registers of 512 threads, which spilled).
+// this row's is used up.  2048 x 32768: 129 us, 4160 GB/s (402 us with the
+// fp32 values in 128 registers of 512 threads, which spilled far more).  At
+// four vectors a thread its 64 registers still spill 160 bytes (bf16; 124 in
+// fp16).
 template <typename E, int NV>
 __global__ void __launch_bounds__(kWideThreads, 1) rms_norm_bwd_wide_kernel(const NormBwdArgs a) {
     extern __shared__ float4 dw[];  // the first halves of all vectors, then the second ones
@@ -383,8 +385,8 @@ __device__ __forceinline__ int4 raw8(const E* p, bool vec, int n) {
     return make_int4(w[0], w[1], w[2], w[3]);
 }
 
-// gelu_tanh adds this to a projection's backward pass: 4098 x 2592 16 us, 7826
-// x 88 10 us (24 and 24 us with 256 columns a block and chunks of 128 rows).
+// gelu_tanh adds this to a projection's backward pass: 4098 x 2592 15 us, 7826
+// x 88 12 us (24 and 24 us with 256 columns a block and chunks of 128 rows).
 template <typename E>
 __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const ActBwdArgs a, int vx, int chunk) {
     __shared__ alignas(16) float part[kActThreads * 8];  // [rows at a time][8 vx columns]

@@ -15,8 +15,8 @@
 //
 // What bounds it: a K block of 64 takes 0.24 us whatever the tokens (four
 // MMAs of 128 rows), a launch 2 us and 0.026 us per token of the tile, and the
-// partials cross the cluster at 1.7 TB/s: 8 x 2048 to 128 with fp32 results 3.7
-// us, 64 x 2048 to 2048 5.7 us, 64 x 4096 to 4096 9.2 us (floor 4.9).
+// partials cross the cluster at 1.7 TB/s: 8 x 2048 to 128 with fp32 results 3.8
+// us, 64 x 2048 to 2048 5.9 us, 64 x 4096 to 4096 9.4 us (floor 4.9).
 //
 // The second product of a feed-forward block starts early: it loads its
 // weights while the first one still runs (programmatic dependent launch) and
