@@ -34,6 +34,10 @@ EXPORTS = [
     "pe_rms_norm", "pe_rms_norm_backward", "pe_rms_norm_backward_workspace", "pe_linear", "pe_linear_backward",
     "pe_linear_backward_workspace", "pe_gated_ffn", "pe_gated_ffn_workspace", "pe_gated_ffn_backward",
     "pe_gated_ffn_backward_workspace", "pe_dense_error", "pe_selftest_dense_waits",
+    "pe_route", "pe_route_workspace", "pe_route_backward", "pe_expand_rows", "pe_combine_rows",
+    "pe_combine_rows_backward", "pe_grouped_linear", "pe_grouped_linear_backward", "pe_grouped_ffn",
+    "pe_grouped_ffn_workspace", "pe_grouped_ffn_backward", "pe_grouped_ffn_backward_workspace",
+    "pe_linear_four_bit", "pe_linear_four_bit_workspace",
 ]
 
 
@@ -113,8 +117,20 @@ def lib() -> ctypes.CDLL:
     L.pe_linear_backward.argtypes = [P, S, P, S, P, P, I, P, P, P, P, N, I, I, I, I, P]
     L.pe_gated_ffn.argtypes = [P, S, P, P, P, S, P, P, I, P, N, I, I, I, I, P]
     L.pe_gated_ffn_backward.argtypes = [P, S, P, S, P, P, P, I, P, P, P, P, N, I, I, I, I, P]
+    L.pe_route.argtypes = [P, S, P, P, P, P, P, N, I, I, I, P]
+    L.pe_route_backward.argtypes = [P, P, P, P, I, I, I, P]
+    L.pe_expand_rows.argtypes = [P, S, P, P, I, I, I, I, I, P]
+    L.pe_combine_rows.argtypes = [P, S, P, P, P, S, P, I, I, I, I, I, P]
+    L.pe_combine_rows_backward.argtypes = [P, S, P, S, P, P, P, P, I, I, I, I, I, P]
+    L.pe_grouped_linear.argtypes = [P, S, P, P, P, I, I, I, I, I, P]
+    L.pe_grouped_linear_backward.argtypes = [P, S, P, S, P, P, P, P, I, I, I, I, I, P]
+    L.pe_grouped_ffn.argtypes = [P, S, P, P, P, P, P, I, P, N, I, I, I, I, I, P]
+    L.pe_grouped_ffn_backward.argtypes = [P, S, P, S, P, P, P, P, I, P, P, P, P, N, I, I, I, I, I, P]
+    L.pe_linear_four_bit.argtypes = [P, S, P, P, P, I, P, P, S, P, I, I, P, N, I, I, I, I, P]
     for name, args in (("pe_rms_norm_backward_workspace", [I, I]), ("pe_linear_backward_workspace", [I, I, I]),
-                       ("pe_gated_ffn_workspace", [I, I]), ("pe_gated_ffn_backward_workspace", [I, I])):
+                       ("pe_gated_ffn_workspace", [I, I]), ("pe_gated_ffn_backward_workspace", [I, I]),
+                       ("pe_route_workspace", [I, I]), ("pe_grouped_ffn_workspace", [I, I]),
+                       ("pe_grouped_ffn_backward_workspace", [I, I]), ("pe_linear_four_bit_workspace", [I, I, I])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = c_size_t
     L.pe_dense_error.argtypes = [POINTER(c_uint32)]

@@ -118,6 +118,11 @@ int split_resident(const SplitShape& s);
 // K, swizzled over 128 bytes.
 bool encode_operand(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8, int box_rows);
 
+// A tensor map of boxes swizzled over 128 bytes: `rank` dimensions, innermost
+// first, strides in bytes of all but the innermost.
+bool encode_boxes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                  bool fp8);
+
 struct NormArgs {
     const void *x, *res, *w;
     int64_t ld_x, ld_res;

@@ -3,6 +3,7 @@
 #include <mutex>
 
 #include "dense.cuh"
+#include "dense_args.h"
 #include "pe_internal.h"
 
 namespace pe {
@@ -11,12 +12,13 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxNormHidden = 32768;
-constexpr int kMaxFeatures = 1 << 24;
 
 __device__ uint32_t g_dense_err;
 
 std::mutex g_mu;
 uint32_t* g_err_ptr[kMaxDevices] = {};
+
+}  // namespace
 
 // Device address of the error word on the current device, looked up once.
 cudaError_t error_word(uint32_t** out) {
@@ -33,22 +35,7 @@ cudaError_t error_word(uint32_t** out) {
     return cudaSuccess;
 }
 
-pe_status bad(const char* msg, pe_status st = PE_ERR_INVALID) {
-    set_thread_error(msg);
-    return st;
-}
-pe_status done(cudaError_t e) {
-    if (!e) return PE_OK;
-    return bad(cudaGetErrorString(e), PE_ERR_CUDA);
-}
-
-bool aligned(const void* p, int to = 16) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
-// what is read and written one element at a time
-bool whole(const float* p) { return aligned(p, sizeof(float)); }
-bool is_elem(int e) { return e == PE_ELEM_BF16 || e == PE_ELEM_F16; }
-bool is_act(int a) { return a >= PE_ACT_NONE && a <= PE_ACT_RELU; }
-bool pitch_ok(int64_t ld, int64_t row, int bytes) { return ld >= row && ld * bytes % 16 == 0 && ld < (int64_t(1) << 36); }
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+namespace {
 
 Product make(const void* a, int64_t lda, int a_mn, const void* b, int64_t ldb, int b_mn, int M, int N, int K) {
     Product p = {};

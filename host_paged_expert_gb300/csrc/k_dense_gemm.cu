@@ -41,6 +41,7 @@
 // warps have too few registers.
 #include "dense.cuh"
 #include "dense_tc.cuh"
+#include "dense_tile.cuh"
 #include "pe_device.cuh"
 
 namespace pe {
@@ -54,7 +55,6 @@ constexpr int threads(int kind, bool fp8, int tn) { return 128 + 32 * epi_warps(
 constexpr int kTile = 256;             // rows of C per CTA pair
 constexpr int kHalf = 128;             // of which each CTA has these
 constexpr int kOperand = kHalf * 128;  // bytes of A's stage in one CTA
-constexpr int kRaster = 8;             // tile rows walked together, so that their B tiles are shared in L2
 constexpr int kMaxStages = 8;
 
 // TN: columns of C per pair (of gate and up together), 256 or 128.
@@ -84,64 +84,6 @@ __device__ __forceinline__ void patch_put(uint8_t* patch, int lane, const uint32
         *reinterpret_cast<uint4*>(patch + lane * 128 + ((j ^ (lane & 7)) << 4)) =
             make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
 }
-// Eight columns 8 c8 .. of row r.
-__device__ __forceinline__ void patch_get(const uint8_t* patch, int r, int c8, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(patch + r * 128 + (((2 * c8) ^ (r & 7)) << 4));
-    const float4 b = *reinterpret_cast<const float4*>(patch + r * 128 + (((2 * c8 + 1) ^ (r & 7)) << 4));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-// What the epilogue of a warp's 32 x 32 block reads, asked for before the
-// block's accumulators are there.
-template <typename E, int KIND>
-struct Ahead {
-    float bias[8];
-    EpiIn in[4];
-    __device__ __forceinline__ void load(const Epi& e, int lane, int row0, int col0) {
-        const int col = col0 + 8 * (lane & 3);
-        epi_cols<E, KIND>(e, col, bias);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) in[it] = epi_load<E, KIND>(e, row0 + it * 8 + (lane >> 2), col);
-    }
-};
-
-template <typename E, int KIND>
-__device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, int lane, int row0, int col0,
-                                          const Ahead<E, KIND>& x) {
-    const int c8 = lane & 3, row = row0 + (lane >> 2), col = col0 + 8 * c8;
-    with_act(e.act, [&](auto act) {
-        constexpr int ACT = decltype(act)::value;
-        if (epi_light<KIND>(e)) {
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                float v[8];
-                patch_get(patch, it * 8 + (lane >> 2), c8, v);
-                epi_store_light<E, ACT>(e, row + it * 8, col, x.bias, x.in[it], v);
-            }
-        } else {
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                float v[8], u[8];
-                patch_get(patch, it * 8 + (lane >> 2), c8, v);
-                if (KIND == EPI_GATED) patch_get(patch + 4096, it * 8 + (lane >> 2), c8, u);
-                epi_store<E, KIND, ACT>(e, row + it * 8, col, x.bias, x.in[it], v, u);
-            }
-        }
-    });
-}
-
-// x / d and x % d without a division: the product with 2^32 / d, rounded down,
-// is the quotient or one less.
-struct Divide {
-    uint32_t d, inv;
-    static Divide by(uint32_t d) { return {d, d > 1 ? (uint32_t)((uint64_t(1) << 32) / d) : 0xffffffffu}; }
-    __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t& rest) const {
-        uint32_t q = __umulhi(x, inv);
-        rest = x - q * d;
-        if (rest >= d) rest -= d, ++q;
-        return q;
-    }
-};
 
 // Products that one launch computes: their tiles are dealt out to the pairs
 // as one sequence, so that a product's last wave is filled by the next one's
@@ -513,18 +455,21 @@ PFN_encode encode_fn() {
 }
 }  // namespace
 
-bool encode_operand(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8, int box_rows) {
+bool encode_boxes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                  bool fp8) {
     auto fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t es = fp8 ? 1 : 2;
-    const cuuint64_t dims[2] = {(cuuint64_t)(mn ? rows : k), (cuuint64_t)(mn ? k : rows)};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
-    const cuuint32_t box[2] = {fp8 ? 128u : 64u, mn ? 64u : (cuuint32_t)box_rows};
-    const cuuint32_t step[2] = {1, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
     // the type only sizes the elements: nothing is converted on the way
-    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
+    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims,
               strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_operand(CUtensorMap* m, const void* base, int64_t ld, int rows, int k, bool mn, bool fp8, int box_rows) {
+    const uint64_t dims[2] = {(uint64_t)(mn ? rows : k), (uint64_t)(mn ? k : rows)}, strides[1] = {(uint64_t)ld * (fp8 ? 1 : 2)};
+    const uint32_t box[2] = {fp8 ? 128u : 64u, mn ? 64u : (uint32_t)box_rows};
+    return encode_boxes(m, base, 2, dims, strides, box, fp8);
 }
 
 cudaError_t launch_pairs(const Product* p, int count, EpiKind kind, int elem, int tn, uint32_t* err, cudaStream_t st,

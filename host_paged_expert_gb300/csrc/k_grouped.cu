@@ -1,0 +1,526 @@
+// Matrix products grouped by expert: rows offsets[g] .. offsets[g + 1] - 1
+// meet the weights of expert g, ragged groups and empty ones among them.
+//
+// Features lie along the MMA's M and rows along its N, which goes in steps of
+// 32: experts of a layer have some tens or hundreds of rows each, of which
+// tiles of 256 rows along M would leave half unused.  Persistent CTA pairs take
+// tiles of 256 features (128 of gate and 128 of up) x up to 256 rows of one
+// group; a group's rows are shared out evenly over the fewest tiles.  Each CTA
+// streams its half of both operands (TMA, 128-byte swizzle) into a ring of
+// stages; one thread of the pair's leader issues the MMAs; accumulators live
+// in TMEM, two buffers of 256 columns, so that the epilogue of a tile runs
+// under the next one's products.  An epilogue warp holds 32 features x 32 rows
+// with a feature per lane and turns them through a patch of shared memory, as
+// the dense products' kernel does, with the block transposed on its way in.
+//
+// Offsets are on the device: every CTA makes a table of the groups' tiles for
+// itself and walks it, 32 groups a look.  They are clamped to [0, rows] and
+// never decrease, whatever they hold, so no access leaves the operands.
+//
+// Weights' gradients (GROUP_WEIGHTS) sum over a group's rows, which lie along
+// K.  The last block of 64 rows runs into the next group, whose rows may hold
+// anything: a warp of each CTA zeroes what is not the group's, in both operands,
+// before the leader may multiply.  The result of an empty group is zeros.
+#include "experts.cuh"
+#include "dense_tc.cuh"
+#include "dense_tile.cuh"
+#include "pe_device.cuh"
+
+namespace pe {
+namespace dense {
+namespace {
+
+constexpr int kEpiWarps = 8, kThreads = 128 + 32 * kEpiWarps;  // warp 0 TMA, 1 MMA, 2 TMEM, 3 clears tails, 4..11 epilogue
+constexpr int kTile = 256, kHalf = 128;  // features (and rows, at most) of a pair's tile, of a CTA's share
+constexpr int kOperand = kHalf * 128, kStage = 2 * kOperand;
+constexpr int kMaxStages = 6;
+constexpr int kBox = 32;  // rows of a copy of the rows' operand
+constexpr int kSmem = 227 * 1024;
+
+constexpr int patch_bytes(int kind) { return kind == GROUP_GATED ? 16384 / 2 : kind == GROUP_WEIGHTS ? 0 : 4096; }  // of a warp
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], raw[kMaxStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+};
+
+struct Work {
+    CUtensorMap w, x;
+    const int32_t* offsets;
+    int groups, rows, features, depth, w_mn;
+    int ftiles;        // tiles along the features
+    int ntiles;        // GROUP_WEIGHTS: along the other side
+    Divide across;     // by ftiles (GROUP_WEIGHTS: by a group's tiles)
+    Divide down;       // GROUP_WEIGHTS: by ftiles
+    int stages;
+    Epi e;
+};
+
+// One tile: group, feature tile, first row (GROUP_WEIGHTS: first column of the
+// other side), the group's end, and the MMA's N.
+struct Tile {
+    int g, f, n0, end, nt;
+    int k0, kn;  // first row along K (GROUP_WEIGHTS; else 0) and the depth
+};
+
+// A pair's way through the tiles, on a table of the groups' offsets and of the
+// tiles up to each group's end.
+template <int KIND>
+struct Walk {
+    int t, i = 0;
+    const int32_t *off, *end;
+    __device__ __forceinline__ bool find(const Work& w, int lane) {
+        if constexpr (KIND == GROUP_WEIGHTS) {
+            return t < w.groups * (w.ftiles * w.ntiles);
+        } else {
+            for (; i < w.groups; i += 32) {
+                const uint32_t past = __ballot_sync(0xffffffffu, i + lane < w.groups && end[i + lane] > t);
+                if (past) {
+                    i += __ffs(past) - 1;
+                    return true;
+                }
+            }
+            return false;
+        }
+    }
+    __device__ __forceinline__ Tile at(const Work& w) const {
+        Tile r;
+        uint32_t rest;
+        if (KIND == GROUP_WEIGHTS) {
+            r.g = (int)w.across((uint32_t)t, rest);
+            uint32_t f;
+            r.n0 = (int)w.down(rest, f) * kTile;
+            r.f = (int)f;
+            r.k0 = off[r.g], r.kn = off[r.g + 1] - r.k0;
+            r.end = w.depth;
+            r.nt = min(kTile, (w.depth - r.n0 + 31) / 32 * 32);
+            return r;
+        }
+        r.g = i;
+        const int r0 = off[i], r1 = off[i + 1], rows = r1 - r0, tiles = (rows + kTile - 1) / kTile;
+        const int x = t - (i ? end[i - 1] : 0);
+        // kRaster row tiles at a time, across all features
+        const int first = (int)w.across((uint32_t)x / kRaster, rest) * kRaster, n = min(kRaster, tiles - first);
+        const uint32_t in = rest * kRaster + x % kRaster;
+        r.f = (int)(n == kRaster ? in / kRaster : in / n);
+        const int per = tiles == 1 ? rows : (rows + tiles - 1) / tiles;
+        r.nt = (per + 31) / 32 * 32;
+        r.n0 = r0 + (first + (int)(in - r.f * n)) * r.nt;
+        r.end = r1;
+        r.k0 = 0, r.kn = w.depth;
+        return r;
+    }
+};
+
+// A warp's 32 features x 32 rows, lane = feature: to the patch, a row of the
+// result per 128 bytes (the layout of patch_get).
+__device__ __forceinline__ void patch_put_t(uint8_t* patch, int lane, const uint32_t (&r)[32]) {
+    const uint32_t in = (lane & 3) * 4, chunk = lane >> 2;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) *reinterpret_cast<uint32_t*>(patch + j * 128 + ((chunk ^ (j & 7)) << 4) + in) = r[j];
+}
+
+// Offsets, clamped and never decreasing, and tiles up to each group's end.
+__device__ __forceinline__ void make_table(const Work& w, int32_t* off, int32_t* end, int lane) {
+    int high = min(max(w.offsets[0], 0), w.rows), tiles = 0;
+    if (lane == 0) off[0] = high;
+    for (int b = 0; b < w.groups; b += 32) {
+        const int i = b + lane;
+        int v = i < w.groups ? min(w.offsets[i + 1], w.rows) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = max(v, n);
+        }
+        v = max(v, high);
+        int before = __shfl_up_sync(0xffffffffu, v, 1);
+        if (lane == 0) before = high;
+        int n = i < w.groups ? (v - before + kTile - 1) / kTile * w.ftiles : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int m = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += m;
+        }
+        n += tiles;
+        if (i < w.groups) off[i + 1] = v, end[i] = n;
+        high = __shfl_sync(0xffffffffu, v, 31);
+        tiles = __shfl_sync(0xffffffffu, n, 31);
+    }
+}
+
+// Named barrier of two warps that exchange gate and up; true if `ok` of both.
+__device__ __forceinline__ bool couple_and(int id, bool ok) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
+        "barrier.cta.red.and.pred.aligned q, %1, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((int)ok)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void couple_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
+
+template <typename E, int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ Work w, uint32_t* err) {
+    constexpr bool WEIGHTS = KIND == GROUP_WEIGHTS, GATED = KIND == GROUP_GATED;
+    constexpr int BK = 64;
+    constexpr int EPI = GATED ? EPI_GATED : KIND == GROUP_GATED_BWD ? EPI_GATED_BWD : EPI_LINEAR;
+    extern __shared__ uint8_t dyn[];
+    __shared__ Shared S;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+    uint8_t* patches = ring + w.stages * kStage;
+    int32_t* off = reinterpret_cast<int32_t*>(patches + kEpiWarps * patch_bytes(KIND));
+    int32_t* end = off + w.groups + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pairs = gridDim.x >> 1;
+    Walk<KIND> walk{(int)(blockIdx.x >> 1), 0, off, end};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < w.stages; ++i) {
+            tc::mbar_init(&S.full[i], WEIGHTS ? 2 : 1);
+            tc::mbar_init(&S.empty[i], 1);
+            tc::mbar_init(&S.raw[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&S.acc_full[i], 1);
+            tc::mbar_init(&S.acc_empty[i], 2 * kEpiWarps);
+        }
+        tc::mbar_init(&S.drain, 1);
+        tc::fence_barrier_init();
+        tc::tma_prefetch(&w.w);
+        tc::tma_prefetch(&w.x);
+    }
+    if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 512);
+    pdl_wait();
+    if (warp == 3) {
+        make_table(w, off, end, lane);
+        pdl_trigger();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_arrive_relaxed();
+    tc::cluster_wait();
+    tc::fence_after_sync();
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 0) {
+        // ---- producer
+        const bool lead = tc::elect_one();
+        const uint32_t bar0 = tc::map_rank(tc::smem_u32(&S.full[0]), 0);  // the leader's
+        uint32_t s = 0, phase = 1;
+        bool ok = true;
+        for (; ok && walk.find(w, lane); walk.t += pairs) {
+            const Tile tl = walk.at(w);
+            const int f0 = GATED ? tl.f * kHalf + (int)rank * 64 : tl.f * kTile + (int)rank * kHalf;
+            const int f1 = GATED ? w.features + f0 : f0 + 64;
+            const int n0 = tl.n0 + (int)rank * (tl.nt / 2), boxes = (tl.nt / 2 + kBox - 1) / kBox;
+            for (int k = 0; k < tl.kn; k += BK) {
+                if (!(ok = tc::mbar_spin(&S.empty[s], phase, err, kPolls))) break;
+                if (lead) {
+                    uint8_t* a = ring + s * kStage;
+                    uint8_t* b = a + kOperand;
+                    const uint32_t bar = bar0 + 8 * s;
+                    if (WEIGHTS) {
+                        const int kk = tl.k0 + k;
+                        if (tl.kn - k >= BK) {
+                            if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * kStage);
+                            else tc::mbar_arrive_cluster(bar);
+                            tc::tma_load_2d_pair(a, &w.w, bar, f0, kk);
+                            tc::tma_load_2d_pair(a + 8192, &w.w, bar, f0 + 64, kk);
+                            tc::tma_load_2d_pair(b, &w.x, bar, n0, kk);
+                            tc::tma_load_2d_pair(b + 8192, &w.x, bar, n0 + 64, kk);
+                        } else {  // for the warp that clears the tail
+                            tc::mbar_arrive_expect_tx(&S.raw[s], kStage);
+                            tc::tma_load_2d(a, &w.w, &S.raw[s], f0, kk);
+                            tc::tma_load_2d(a + 8192, &w.w, &S.raw[s], f0 + 64, kk);
+                            tc::tma_load_2d(b, &w.x, &S.raw[s], n0, kk);
+                            tc::tma_load_2d(b + 8192, &w.x, &S.raw[s], n0 + 64, kk);
+                        }
+                    } else {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * (kOperand + boxes * kBox * 128));
+                        if (w.w_mn) {
+                            tc::tma_load_3d_pair(a, &w.w, bar, f0, k, tl.g);
+                            tc::tma_load_3d_pair(a + 8192, &w.w, bar, f1, k, tl.g);
+                        } else {
+                            tc::tma_load_3d_pair(a, &w.w, bar, k, f0, tl.g);
+                            tc::tma_load_3d_pair(a + 8192, &w.w, bar, k, f1, tl.g);
+                        }
+                        for (int i = 0; i < boxes; ++i) tc::tma_load_2d_pair(b + i * kBox * 128, &w.x, bar, k, n0 + i * kBox);
+                    }
+                }
+                __syncwarp();
+                if (++s == (uint32_t)w.stages) s = 0, phase ^= 1;
+            }
+        }
+        // The leader's MMAs arrive on this CTA's barriers: stay until the last of
+        // them have (a stage never used passes at once).
+        for (int i = 0; ok && i < w.stages; ++i) {
+            ok = tc::mbar_spin(&S.empty[s], phase, err, kPolls);
+            if (++s == (uint32_t)w.stages) s = 0, phase ^= 1;
+        }
+        if (!ok) tc::settle();  // copies may be on their way
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMA issuer
+        const bool lead = tc::elect_one();
+        constexpr int FMT = std::is_same<E, __nv_bfloat16>::value ? 1 : 0;
+        const int a_mn = WEIGHTS || w.w_mn, b_mn = WEIGHTS;
+        const uint32_t astep = (a_mn ? 2048 : 32) >> 4, bstep = (b_mn ? 2048 : 32) >> 4;
+        const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), a_mn), b0 = tc::operand_desc(tc::smem_u32(ring) + kOperand, b_mn);
+        uint32_t s = 0, phase = 0, buf = 0, buf_phase = 1;
+        bool ok = true;
+        for (; ok && walk.find(w, lane); walk.t += pairs) {
+            const Tile tl = walk.at(w);
+            if (tl.kn <= 0) continue;  // zeros
+            const uint32_t id = tc::idesc(FMT, a_mn, b_mn, kTile, tl.nt);
+            if (!(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, kPolls))) break;
+            for (int k = 0; k < tl.kn; k += BK) {
+                if (!(ok = WEIGHTS ? tc::mbar_spin_cluster(&S.full[s], phase, err, kPolls) : tc::mbar_spin(&S.full[s], phase, err, kPolls))) break;
+                tc::fence_after_sync();
+                if (lead) {
+                    const uint64_t a = a0 + s * (kStage >> 4), b = b0 + s * (kStage >> 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!WEIGHTS || k + 16 * i < tl.kn)
+                            tc::mma<true, false>(tmem + buf * kTile, a + i * astep, b + i * bstep, id, k || i);
+                    tc::mma_commit_pair(&S.empty[s]);
+                    if (k + BK >= tl.kn) tc::mma_commit_pair(&S.acc_full[buf]);
+                }
+                __syncwarp();
+                if (++s == (uint32_t)w.stages) s = 0, phase ^= 1;
+            }
+            buf ^= 1;
+            if (buf == 0) buf_phase ^= 1;
+        }
+        // the other CTA's epilogue warps arrive here too: stay until the last of them have
+        for (int i = 0; ok && i < 2; ++i) {
+            ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, kPolls);
+            buf ^= 1;
+            if (buf == 0) buf_phase ^= 1;
+        }
+        if (!ok) {  // the MMAs already issued read shared memory and write TMEM
+            if (lead) tc::mma_commit_pair_here(&S.drain);
+            tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, tc::kLeavePolls);
+        }
+    } else if (WEIGHTS && warp == 3) {
+        // ---- tails: rows of the next group, up to the MMA's step of 16, become zeros
+        const uint32_t bar0 = tc::map_rank(tc::smem_u32(&S.full[0]), 0);
+        uint32_t s = 0, phases = 0;
+        bool ok = true;
+        for (; ok && walk.find(w, lane); walk.t += pairs) {
+            const Tile tl = walk.at(w);
+            const int blocks = (tl.kn + BK - 1) / BK, rem = tl.kn % BK;
+            if (rem) {
+                const uint32_t at = (s + blocks - 1) % w.stages;
+                if (!(ok = tc::mbar_spin(&S.raw[at], phases >> at & 1, err, kPolls))) break;
+                phases ^= 1u << at;
+                // a row along K is 128 bytes of each of four boxes
+                uint8_t* to = ring + at * kStage + (lane >> 3) * 8192 + (lane & 7) * 16;
+                for (int r = rem; r < (rem + 15) / 16 * 16; ++r) *reinterpret_cast<uint4*>(to + r * 128) = make_uint4(0, 0, 0, 0);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster_release(bar0 + 8 * at);
+            }
+            s = (s + blocks) % w.stages;
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue
+        const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t release = tc::map_rank(tc::smem_u32(&S.acc_empty[0]), 0);  // of the pair's leader
+        uint32_t use_acc = 0;
+        bool ok = true;
+        for (; walk.find(w, lane); walk.t += pairs) {
+            const Tile tl = walk.at(w);
+            const uint32_t buf = use_acc & 1, at = lanes + buf * kTile;
+            auto let_go = [&] {
+                tc::fence_before_sync();
+                if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
+            };
+            if constexpr (WEIGHTS) {
+                const int m = tl.f * kTile + (int)rank * kHalf + quarter * 32 + lane, c0 = half * kHalf;
+                E* row = static_cast<E*>(w.e.out) + ((int64_t)tl.g * w.features + m) * w.depth;
+                if (tl.kn > 0) {
+                    if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, kPolls))) break;
+                    ++use_acc;
+                    tc::fence_after_sync();
+                }
+#pragma unroll 1
+                for (int c = 0; c < kHalf / 32; ++c) {
+                    uint32_t r[32];
+                    if (tl.kn > 0) {
+                        tc::tmem_ld32(at + c0 + c * 32, r);
+                        tc::tmem_ld_wait(r);
+                        if (c == kHalf / 32 - 1) let_go();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = 0;
+                    }
+                    if (m < w.features)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int col = tl.n0 + c0 + c * 32 + 8 * j;
+                            float v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
+                            if (col < w.depth) store8(row + col, true, 8, v);
+                        }
+                }
+            } else {
+                Epi e = w.e;
+                e.rows = tl.end;
+                const int live = min(tl.nt, tl.end - tl.n0);  // rows of this tile
+                ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, kPolls);
+                const int couple = 1 + half * 2 + (quarter & 1);
+                if (GATED) ok = couple_and(couple, ok);
+                if (!ok) break;
+                ++use_acc;
+                tc::fence_after_sync();
+                if (half * 32 >= live) let_go();
+                if constexpr (GATED) {
+                    const int f = tl.f * kHalf + (int)rank * 64 + (quarter & 1) * 32, part = quarter >> 1;
+                    uint8_t* mine = patches + (couple - 1) * (2 * patch_bytes(KIND));
+                    uint32_t turn = 0;
+#pragma unroll 1
+                    for (int c = half * 32; c < live; c += 64, turn ^= 8192) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(at + c, r);
+                        tc::tmem_ld_wait(r);
+                        if (c + 64 >= live) let_go();
+                        patch_put_t(mine + turn + part * 4096, lane, r);
+                        couple_sync(couple);  // two patches in turn: the partner may still read the other one
+                        const int c8 = lane & 3, col = f + 8 * c8;
+                        with_act(e.act, [&](auto act) {
+#pragma unroll
+                            for (int it = 0; it < 2; ++it) {
+                                const int rr = (2 * part + it) * 8 + (lane >> 2);
+                                float v[8], u[8];
+                                patch_get(mine + turn, rr, c8, v);
+                                patch_get(mine + turn + 4096, rr, c8, u);
+                                epi_store<E, EPI_GATED, decltype(act)::value>(e, tl.n0 + c + rr, col, v, EpiIn{}, v, u);
+                            }
+                        });
+                    }
+                    couple_sync(couple);  // nor may the next tile's first patch meet its readers
+                } else {
+                    const int f = tl.f * kTile + (int)rank * kHalf + quarter * 32;
+                    uint8_t* patch = patches + ew * patch_bytes(KIND);
+#pragma unroll 1
+                    for (int c = half * 32; c < live; c += 64) {
+                        Ahead<E, EPI> x;
+                        x.load(e, lane, tl.n0 + c, f);
+                        uint32_t r[32];
+                        tc::tmem_ld32(at + c, r);
+                        tc::tmem_ld_wait(r);
+                        if (c + 64 >= live) let_go();
+                        __syncwarp();  // the patch's last readers are done
+                        patch_put_t(patch, lane, r);
+                        __syncwarp();
+                        patch_out<E, EPI>(e, patch, lane, tl.n0 + c, f, x);
+                    }
+                }
+            }
+        }
+    }
+    // neither CTA leaves, and no TMEM is freed, while the other may still use it
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_arrive_relaxed();
+    tc::cluster_wait();
+    tc::fence_after_sync();
+    if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+int table_bytes(int groups) { return 4 * (2 * groups + 1); }
+// Stages of the ring that fit next to the patches and the table.
+int stages_of(GroupKind kind, int groups) {
+    const int room = kSmem - 1024 - (int)sizeof(Shared) - kEpiWarps * patch_bytes(kind) - table_bytes(groups);
+    return room / kStage < kMaxStages ? room / kStage : kMaxStages;
+}
+
+// Pairs that the device holds at once, looked up once per kernel.
+template <typename E, int KIND>
+cudaError_t resident_pairs(int* out) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    int n = dev < 64 ? known[dev].load() : 0;
+    if (!n) {
+        auto k = grouped_kernel<E, KIND>;
+        const int bytes = kSmem - (int)sizeof(Shared);
+        if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = bytes;
+        if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, k, &cfg)) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        if (dev < 64) known[dev].store(n);
+    }
+    *out = n;
+    return cudaSuccess;
+}
+
+template <typename E, int KIND>
+cudaError_t launch(const Grouped& p, uint32_t* err, cudaStream_t st) {
+    constexpr bool WEIGHTS = KIND == GROUP_WEIGHTS;
+    constexpr int NF = KIND == GROUP_GATED ? kHalf : kTile;
+    Work w = {};
+    if (WEIGHTS) {
+        if (!encode_operand(&w.w, p.w, p.ld_w, p.features, p.rows, true, false, 0) ||
+            !encode_operand(&w.x, p.x, p.ld_x, p.depth, p.rows, true, false, 0))
+            return cudaErrorInvalidValue;
+    } else {
+        const uint64_t lines = (uint64_t)p.features * (KIND == GROUP_GATED ? 2 : 1), k = p.depth;
+        const uint64_t dims[3] = {p.w_mn ? lines : k, p.w_mn ? k : lines, (uint64_t)p.groups};
+        const uint64_t strides[2] = {2 * dims[0], 2 * dims[0] * dims[1]};
+        const uint32_t box[3] = {64, 64, 1};
+        if (!encode_boxes(&w.w, p.w, 3, dims, strides, box, false) ||
+            !encode_operand(&w.x, p.x, p.ld_x, p.rows, p.depth, false, false, kBox))
+            return cudaErrorInvalidValue;
+    }
+    w.offsets = p.offsets;
+    w.groups = p.groups;
+    w.rows = p.rows;
+    w.features = p.features;
+    w.depth = p.depth;
+    w.w_mn = p.w_mn;
+    w.ftiles = (p.features + NF - 1) / NF;
+    w.ntiles = (p.depth + kTile - 1) / kTile;
+    w.across = Divide::by(WEIGHTS ? w.ftiles * w.ntiles : w.ftiles);
+    w.down = Divide::by(w.ftiles);
+    w.stages = stages_of((GroupKind)KIND, p.groups);
+    w.e = p.e;
+    w.e.cols = p.features;
+    w.e.vec = 1;
+    // no more tiles than these, wherever the offsets lie
+    const long long most = WEIGHTS ? (long long)p.groups * w.ftiles * w.ntiles
+                                   : ((long long)p.rows / kTile + (p.groups < p.rows ? p.groups : p.rows)) * w.ftiles;
+    if (most > INT_MAX / 2 || w.stages < 2) return cudaErrorInvalidValue;
+    int pairs = 0;
+    if (cudaError_t e = resident_pairs<E, KIND>(&pairs)) return e;
+    if (most < pairs) pairs = (int)most;
+    const int bytes = 1024 + w.stages * kStage + kEpiWarps * patch_bytes(KIND) + table_bytes(p.groups);
+    return launch_pdl(grouped_kernel<E, KIND>, dim3(2 * pairs), dim3(kThreads), bytes, st, w, err);
+}
+
+template <typename E>
+cudaError_t launch_kind(const Grouped& p, GroupKind kind, uint32_t* err, cudaStream_t st) {
+    switch (kind) {
+        case GROUP_ROWS: return launch<E, GROUP_ROWS>(p, err, st);
+        case GROUP_GATED: return launch<E, GROUP_GATED>(p, err, st);
+        case GROUP_GATED_BWD: return launch<E, GROUP_GATED_BWD>(p, err, st);
+        default: return launch<E, GROUP_WEIGHTS>(p, err, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_grouped(const Grouped& p, GroupKind kind, int elem, uint32_t* err, cudaStream_t st) {
+    return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, err, st) : launch_kind<__half>(p, kind, err, st);
+}
+
+}  // namespace dense
+}  // namespace pe

@@ -468,6 +468,114 @@ pe_status pe_gated_ffn_backward(const void* dy, int64_t dy_stride, const void* x
                                 void* workspace, size_t workspace_bytes, int32_t rows, int32_t hidden,
                                 int32_t intermediate, int32_t elem, void* stream);
 
+/* ---- A layer whose experts are resident ----------------------------------
+ *
+ * Route, rows to their experts, products grouped by expert, rows back: what a
+ * mixture-of-experts layer runs when its experts are trained, or all sit in
+ * device memory (pe_forward is the layer whose experts are paged).  The
+ * conventions are those of the dense operators above.  Indices are 32-bit and
+ * on the device; none of them, whatever it holds, makes a call leave its
+ * operands.  A "row" is one entry (token, i) of the top-k choice, in the order
+ * sorted by expert. */
+
+/* The top_k experts of each token, by logit (ties to the lower expert, NaN as
+ * -infinity, as pe_forward routes), and each entry's row.
+ *   logits: [tokens, experts] fp32, row pitch logits_stride;
+ *   ids: [tokens, top_k] experts in falling order of their logits;
+ *   weights: [tokens, top_k] softmax over the chosen logits (logits of
+ *     +infinity, or only of -infinity, share the weight evenly);
+ *   offsets: [experts + 1]: the rows of expert e are offsets[e] .. offsets[e+1] - 1;
+ *   place: [tokens, top_k] the row of each entry: rows are sorted by expert, and
+ *     by token within an expert.
+ * top_k at most 32, experts at most 1024, tokens * top_k at most 2^31 - 1.
+ * workspace: pe_route_workspace(tokens, experts) bytes. */
+size_t pe_route_workspace(int32_t tokens, int32_t experts);
+pe_status pe_route(const float* logits, int64_t logits_stride, int32_t* ids, float* weights, int32_t* offsets,
+                   int32_t* place, void* workspace, size_t workspace_bytes, int32_t tokens, int32_t top_k,
+                   int32_t experts, void* stream);
+
+/* The gradient of the logits: w_i (dw_i - sum_j w_j dw_j) at expert ids[t, i],
+ * zero elsewhere; an expert that a token names twice gets the sum, an id that is
+ * no expert's is left out.  dlogits: [tokens, experts] fp32, 16-byte aligned. */
+pe_status pe_route_backward(const float* dweights, const float* weights, const int32_t* ids, float* dlogits,
+                            int32_t tokens, int32_t top_k, int32_t experts, void* stream);
+
+/* out[place[t, i]] = x[t] for every entry.  out: [rows, hidden].  Entries whose
+ * place is outside [0, rows) are left out, rows that no entry names stay as
+ * they were; no two entries may name the same row.  Its gradient is
+ * pe_combine_rows without weights. */
+pe_status pe_expand_rows(const void* x, int64_t x_stride, const int32_t* place, void* out, int32_t tokens,
+                         int32_t top_k, int32_t rows, int32_t hidden, int32_t elem, void* stream);
+
+/* out[t] = sum_i weights[t, i] y[place[t, i]] + residual[t], added in the order
+ * of i.  weights: [tokens, top_k] fp32, or NULL for ones; entries whose place is
+ * outside [0, rows) are left out. */
+pe_status pe_combine_rows(const void* y, int64_t y_stride, const int32_t* place, const float* weights,
+                          const void* residual, int64_t residual_stride, void* out, int32_t tokens, int32_t top_k,
+                          int32_t rows, int32_t hidden, int32_t elem, void* stream);
+
+/* Its gradients: dy[place[t, i]] = weights[t, i] dout[t] and dweights[t, i] =
+ * <dout[t], y[place[t, i]]> (0 for an entry that is left out).  Rows that no
+ * entry names stay as they were; no two entries may name the same row.
+ * dweights may be NULL, and y with it.  The residual's gradient is dout. */
+pe_status pe_combine_rows_backward(const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
+                                   const int32_t* place, const float* weights, void* dy, float* dweights,
+                                   int32_t tokens, int32_t top_k, int32_t rows, int32_t hidden, int32_t elem,
+                                   void* stream);
+
+/* out[r] = x[r] weight[g]^T for rows offsets[g] <= r < offsets[g + 1].
+ *   weight: [groups, out, in]; offsets: [groups + 1], not decreasing.  A group
+ *   may be empty; rows in no group stay as they were.
+ * in, out: multiples of 8; groups at most 1024. */
+pe_status pe_grouped_linear(const void* x, int64_t x_stride, const void* weight, const int32_t* offsets, void* out,
+                            int32_t rows, int32_t groups, int32_t in_features, int32_t out_features, int32_t elem,
+                            void* stream);
+
+/* Its gradients: dx[r] = dy[r] weight[g] (rows in no group stay as they were),
+ * dweight[g] = sum over the group's rows of dy[r]^T x[r] (zeros for an empty
+ * group); either may be NULL. */
+pe_status pe_grouped_linear_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                     const void* weight, const int32_t* offsets, void* dx, void* dweight,
+                                     int32_t rows, int32_t groups, int32_t in_features, int32_t out_features,
+                                     int32_t elem, void* stream);
+
+/* pe_gated_ffn with the weights of each group: w13 [groups, 2 intermediate,
+ * hidden], w2 [groups, hidden, intermediate]; no residual.  keep: [rows,
+ * 2 intermediate] or NULL.  Rows in no group stay as they were.
+ * workspace: pe_grouped_ffn_workspace(rows, intermediate) bytes. */
+size_t pe_grouped_ffn_workspace(int32_t rows, int32_t intermediate);
+pe_status pe_grouped_ffn(const void* x, int64_t x_stride, const void* w13, const void* w2, const int32_t* offsets,
+                         void* out, void* keep, int32_t act, void* workspace, size_t workspace_bytes, int32_t rows,
+                         int32_t groups, int32_t hidden, int32_t intermediate, int32_t elem, void* stream);
+
+/* Its gradients, as pe_gated_ffn_backward for each group; dx, dw13 and dw2 may
+ * be NULL.  workspace: pe_grouped_ffn_backward_workspace(rows, intermediate). */
+size_t pe_grouped_ffn_backward_workspace(int32_t rows, int32_t intermediate);
+pe_status pe_grouped_ffn_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* w13,
+                                  const void* w2, const void* keep, const int32_t* offsets, int32_t act, void* dx,
+                                  void* dw13, void* dw2, void* workspace, size_t workspace_bytes, int32_t rows,
+                                  int32_t groups, int32_t hidden, int32_t intermediate, int32_t elem, void* stream);
+
+/* pe_linear with 4-bit weights: out = act(x W^T + bias) + residual.
+ *   format: PE_INT4_GPTQ, PE_MXFP4 or PE_NVFP4; W[n, k] = code * scale with
+ *   codes: [out, in / 2] bytes, input 2j in the low nibble of byte j, as in an
+ *     expert row;
+ *   scales: int4: fp16 [out, ceil(in/128)], W = (code - 8) * scale; MXFP4: E8M0
+ *     [out, in/32]; NVFP4: E4M3 [out, in/16], times tensor_scale[0] (device; NULL
+ *     for the other formats).
+ * Up to 64 rows the weights are streamed and used unrounded (with fp16, MXFP4
+ * scales above 2^16 count as 2^16 and are lost below 2^-23; with bf16 they are
+ * cut at 2^120); above, they are unpacked to elem in the workspace first:
+ * int4's and NVFP4's products with their scales are rounded there.
+ * in: a multiple of 32.
+ * workspace: pe_linear_four_bit_workspace(rows, in, out) bytes. */
+size_t pe_linear_four_bit_workspace(int32_t rows, int32_t in_features, int32_t out_features);
+pe_status pe_linear_four_bit(const void* x, int64_t x_stride, const void* codes, const void* scales,
+                             const float* tensor_scale, int32_t format, const void* bias, const void* residual,
+                             int64_t residual_stride, void* out, int32_t out_elem, int32_t act, void* workspace,
+                             size_t workspace_bytes, int32_t rows, int32_t in_features, int32_t out_features,
+                             int32_t elem, void* stream);
+
 /* Error word of the dense operators on the current device: 0, or
  * PE_DEVERR_TIMEOUT once a bounded wait inside one of their kernels gave up
  * (that call's results are then incomplete).  Sticky.  Synchronises the
