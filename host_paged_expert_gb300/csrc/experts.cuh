@@ -57,8 +57,8 @@ cudaError_t launch_combine_bwd(const RowsArgs& a, int elem, cudaStream_t st);
 // leaves [0, rows] is clamped.  Features lie along the MMA's M.
 enum GroupKind {
     GROUP_ROWS = 0,      // out[r, f] = sum_k w[g][f, k] x[r, k]  (w_mn: w[g][k, f])
-    GROUP_GATED = 1,     // the same with gate and up rows of w, act(gate) * up; optionally both kept
-    GROUP_GATED_BWD = 2, // dh as GROUP_ROWS, then the gradients of gate and up, and h
+    GROUP_GATED = 1,     // the same with gate and up rows of w, act(gate) * up; optionally both kept, in fp32
+    GROUP_GATED_BWD = 2, // dh as GROUP_ROWS, then the gradients of gate and up, and h, from what was kept
     GROUP_WEIGHTS = 3,   // out[g][m, n] = sum over the group's rows of w[r, m] x[r, n]
 };
 struct Grouped {

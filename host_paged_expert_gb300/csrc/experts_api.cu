@@ -256,7 +256,8 @@ extern "C" pe_status pe_grouped_ffn(const void* x, int64_t x_stride, const void*
     if (!e) {
         Grouped p = product(w13, 0, x, x_stride, offsets, rows, groups, intermediate, hidden);
         p.e.act = act;
-        // h is rounded to 16 bits, the type that the second product's MMA takes
+        // h is rounded to 16 bits, the type that the second product's MMA takes; what is
+        // kept is not (16 bits would add as much again to the gradients' error)
         p.e.out = workspace;
         p.e.ld_out = intermediate;
         p.e.keep = keep;

@@ -37,7 +37,7 @@ constexpr int kMaxStages = 6;
 constexpr int kBox = 32;  // rows of a copy of the rows' operand
 constexpr int kSmem = 227 * 1024;
 
-constexpr int patch_bytes(int kind) { return kind == GROUP_GATED ? 16384 / 2 : kind == GROUP_WEIGHTS ? 0 : 4096; }  // of a warp
+constexpr int patch_bytes(int kind) { return kind == GROUP_GATED ? 8192 : 4096; }  // of a warp
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], raw[kMaxStages], acc_full[2], acc_empty[2], drain;
@@ -46,6 +46,7 @@ struct Shared {
 
 struct Work {
     CUtensorMap w, x;
+    CUtensorMap w_tail, x_tail, out;  // GROUP_WEIGHTS: boxes of 16 rows, the result
     const int32_t* offsets;
     int groups, rows, features, depth, w_mn;
     int ftiles;        // tiles along the features
@@ -63,18 +64,31 @@ struct Tile {
     int k0, kn;  // first row along K (GROUP_WEIGHTS; else 0) and the depth
 };
 
-// A pair's way through the tiles, on a table of the groups' offsets and of the
-// tiles up to each group's end.
+// Rows of a group's tiles: shared out evenly over the fewest of them.
+__device__ __forceinline__ int tile_rows(int rows) {
+    const int tiles = (rows + kTile - 1) / kTile;
+    return tiles <= 1 ? (rows + 31) / 32 * 32 : ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+}
+
+struct Table {
+    int32_t *off, *end;  // rows ahead of each group; tiles up to each group's end
+};
+
+// A pair's way through the tiles: every `pairs`-th, group by group.  (Dealt out
+// evenly by size, from large to small or large and small in turn, they took as
+// long or longer: it is the mixture of tiles bound by the tensor cores with
+// tiles bound by their stores that counts.)
 template <int KIND>
 struct Walk {
-    int t, i = 0;
-    const int32_t *off, *end;
+    Table tab;
+    int t, pairs, i = 0;
+    __device__ __forceinline__ void next() { t += pairs; }
     __device__ __forceinline__ bool find(const Work& w, int lane) {
         if constexpr (KIND == GROUP_WEIGHTS) {
             return t < w.groups * (w.ftiles * w.ntiles);
         } else {
             for (; i < w.groups; i += 32) {
-                const uint32_t past = __ballot_sync(0xffffffffu, i + lane < w.groups && end[i + lane] > t);
+                const uint32_t past = __ballot_sync(0xffffffffu, i + lane < w.groups && tab.end[i + lane] > t);
                 if (past) {
                     i += __ffs(past) - 1;
                     return true;
@@ -91,26 +105,34 @@ struct Walk {
             uint32_t f;
             r.n0 = (int)w.down(rest, f) * kTile;
             r.f = (int)f;
-            r.k0 = off[r.g], r.kn = off[r.g + 1] - r.k0;
+            r.k0 = tab.off[r.g], r.kn = tab.off[r.g + 1] - r.k0;
             r.end = w.depth;
             r.nt = min(kTile, (w.depth - r.n0 + 31) / 32 * 32);
             return r;
         }
         r.g = i;
-        const int r0 = off[i], r1 = off[i + 1], rows = r1 - r0, tiles = (rows + kTile - 1) / kTile;
-        const int x = t - (i ? end[i - 1] : 0);
+        const int r0 = tab.off[i], r1 = tab.off[i + 1], rows = r1 - r0, tiles = (rows + kTile - 1) / kTile;
+        const int x = t - (i ? tab.end[i - 1] : 0);
         // kRaster row tiles at a time, across all features
         const int first = (int)w.across((uint32_t)x / kRaster, rest) * kRaster, n = min(kRaster, tiles - first);
         const uint32_t in = rest * kRaster + x % kRaster;
         r.f = (int)(n == kRaster ? in / kRaster : in / n);
-        const int per = tiles == 1 ? rows : (rows + tiles - 1) / tiles;
-        r.nt = (per + 31) / 32 * 32;
+        r.nt = tile_rows(rows);
         r.n0 = r0 + (first + (int)(in - r.f * n)) * r.nt;
         r.end = r1;
         r.k0 = 0, r.kn = w.depth;
         return r;
     }
 };
+
+// A tail's block is copied kEarly blocks ahead of its turn, so that it is clear
+// by then: the place among a tile's copies of its last block.
+constexpr int kEarly = 3;
+template <bool WEIGHTS>
+__device__ __forceinline__ int early_at(int depth) {
+    const int last = (depth + 63) / 64 - 1;
+    return WEIGHTS && depth % 64 ? max(0, last - kEarly) : last;
+}
 
 // A warp's 32 features x 32 rows, lane = feature: to the patch, a row of the
 // result per 128 bytes (the layout of patch_get).
@@ -120,10 +142,11 @@ __device__ __forceinline__ void patch_put_t(uint8_t* patch, int lane, const uint
     for (int j = 0; j < 32; ++j) *reinterpret_cast<uint32_t*>(patch + j * 128 + ((chunk ^ (j & 7)) << 4) + in) = r[j];
 }
 
-// Offsets, clamped and never decreasing, and tiles up to each group's end.
-__device__ __forceinline__ void make_table(const Work& w, int32_t* off, int32_t* end, int lane) {
+// By one warp: offsets, clamped and never decreasing, and tiles up to each
+// group's end.
+__device__ __forceinline__ void make_table(const Work& w, const Table& tab, int lane) {
     int high = min(max(w.offsets[0], 0), w.rows), tiles = 0;
-    if (lane == 0) off[0] = high;
+    if (lane == 0) tab.off[0] = high;
     for (int b = 0; b < w.groups; b += 32) {
         const int i = b + lane;
         int v = i < w.groups ? min(w.offsets[i + 1], w.rows) : 0;
@@ -142,7 +165,7 @@ __device__ __forceinline__ void make_table(const Work& w, int32_t* off, int32_t*
             if (lane >= o) n += m;
         }
         n += tiles;
-        if (i < w.groups) off[i + 1] = v, end[i] = n;
+        if (i < w.groups) tab.off[i + 1] = v, tab.end[i] = n;
         high = __shfl_sync(0xffffffffu, v, 31);
         tiles = __shfl_sync(0xffffffffu, n, 31);
     }
@@ -161,21 +184,79 @@ __device__ __forceinline__ bool couple_and(int id, bool ok) {
 }
 __device__ __forceinline__ void couple_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
 
+// What the epilogue of a warp's 32 x 32 block reads, asked for before the
+// block's accumulators are there, and what it does with them: nothing but
+// rounding, or (GROUP_GATED_BWD) the gradients of gate and up and h from dh and
+// the fp32 gate and up that the forward call kept.
+template <typename E, int KIND>
+struct Before {
+    __device__ __forceinline__ void load(const Epi&, int, int, int) {}
+    __device__ __forceinline__ void out(const Epi& e, const uint8_t* patch, int lane, int row0, int col0) const {
+        const int c8 = lane & 3, col = col0 + 8 * c8;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int rr = it * 8 + (lane >> 2), row = row0 + rr;
+            float v[8];
+            patch_get(patch, rr, c8, v);
+            if (row < e.rows && col < e.cols) store8(static_cast<E*>(e.out) + row * e.ld_out + col, true, 8, v);
+        }
+    }
+};
+template <typename E>
+struct Before<E, GROUP_GATED_BWD> {
+    float4 g[4][2], u[4][2];
+    __device__ __forceinline__ void load(const Epi& e, int lane, int row0, int col0) {
+        const int col = col0 + 8 * (lane & 3);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int row = row0 + it * 8 + (lane >> 2);
+            if (row >= e.rows || col >= e.cols) continue;
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.gu) + row * e.ld_keep + col);
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(e.gu) + row * e.ld_keep + e.cols + col);
+            g[it][0] = p[0], g[it][1] = p[1], u[it][0] = q[0], u[it][1] = q[1];
+        }
+    }
+    __device__ __forceinline__ void out(const Epi& e, const uint8_t* patch, int lane, int row0, int col0) const {
+        const int c8 = lane & 3, col = col0 + 8 * c8;
+        with_act(e.act, [&](auto act) {
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int rr = it * 8 + (lane >> 2), row = row0 + rr;
+                if (row >= e.rows || col >= e.cols) continue;
+                float v[8];
+                patch_get(patch, rr, c8, v);
+                float a[8] = {g[it][0].x, g[it][0].y, g[it][0].z, g[it][0].w, g[it][1].x, g[it][1].y, g[it][1].z, g[it][1].w};
+                float b[8] = {u[it][0].x, u[it][0].y, u[it][0].z, u[it][0].w, u[it][1].x, u[it][1].y, u[it][1].z, u[it][1].w};
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a[i] = act_both(decltype(act)::value, a[i], d[i]);
+                    d[i] *= v[i] * b[i];  // dg
+                    b[i] *= a[i];         // h
+                    a[i] *= v[i];         // du
+                }
+                E* o = static_cast<E*>(e.out) + row * e.ld_out + col;
+                store8(o, true, 8, d);
+                store8(o + e.cols, true, 8, a);
+                if (e.h) store8(static_cast<E*>(e.h) + row * (int64_t)e.cols + col, true, 8, b);
+            }
+        });
+    }
+};
+
 template <typename E, int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ Work w, uint32_t* err) {
     constexpr bool WEIGHTS = KIND == GROUP_WEIGHTS, GATED = KIND == GROUP_GATED;
     constexpr int BK = 64;
-    constexpr int EPI = GATED ? EPI_GATED : KIND == GROUP_GATED_BWD ? EPI_GATED_BWD : EPI_LINEAR;
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     uint8_t* patches = ring + w.stages * kStage;
     int32_t* off = reinterpret_cast<int32_t*>(patches + kEpiWarps * patch_bytes(KIND));
-    int32_t* end = off + w.groups + 1;
+    const Table tab = {off, off + w.groups + 1};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
-    const int pairs = gridDim.x >> 1;
-    Walk<KIND> walk{(int)(blockIdx.x >> 1), 0, off, end};
+    Walk<KIND> walk{tab, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1)};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < w.stages; ++i) {
@@ -195,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
     if (warp == 2) tc::tmem_alloc_pair(&S.tmem, 512);
     pdl_wait();
     if (warp == 3) {
-        make_table(w, off, end, lane);
+        make_table(w, tab, lane);
         pdl_trigger();
     }
     tc::fence_before_sync();
@@ -211,12 +292,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         const uint32_t bar0 = tc::map_rank(tc::smem_u32(&S.full[0]), 0);  // the leader's
         uint32_t s = 0, phase = 1;
         bool ok = true;
-        for (; ok && walk.find(w, lane); walk.t += pairs) {
+        for (; ok && walk.find(w, lane); walk.next()) {
             const Tile tl = walk.at(w);
             const int f0 = GATED ? tl.f * kHalf + (int)rank * 64 : tl.f * kTile + (int)rank * kHalf;
             const int f1 = GATED ? w.features + f0 : f0 + 64;
             const int n0 = tl.n0 + (int)rank * (tl.nt / 2), boxes = (tl.nt / 2 + kBox - 1) / kBox;
-            for (int k = 0; k < tl.kn; k += BK) {
+            const int blocks = (tl.kn + BK - 1) / BK, early = early_at<WEIGHTS>(tl.kn);
+            for (int j = 0; j < blocks; ++j) {
+                const int k = (!WEIGHTS || j < early ? j : j == early ? blocks - 1 : j - 1) * BK;
                 if (!(ok = tc::mbar_spin(&S.empty[s], phase, err, kPolls))) break;
                 if (lead) {
                     uint8_t* a = ring + s * kStage;
@@ -231,12 +314,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                             tc::tma_load_2d_pair(a + 8192, &w.w, bar, f0 + 64, kk);
                             tc::tma_load_2d_pair(b, &w.x, bar, n0, kk);
                             tc::tma_load_2d_pair(b + 8192, &w.x, bar, n0 + 64, kk);
-                        } else {  // for the warp that clears the tail
-                            tc::mbar_arrive_expect_tx(&S.raw[s], kStage);
-                            tc::tma_load_2d(a, &w.w, &S.raw[s], f0, kk);
-                            tc::tma_load_2d(a + 8192, &w.w, &S.raw[s], f0 + 64, kk);
-                            tc::tma_load_2d(b, &w.x, &S.raw[s], n0, kk);
-                            tc::tma_load_2d(b + 8192, &w.x, &S.raw[s], n0 + 64, kk);
+                        } else {  // for the warp that clears the tail: as many rows as the MMAs will read
+                            const int steps = (tl.kn - k + 15) / 16;
+                            tc::mbar_arrive_expect_tx(&S.raw[s], steps * 4 * 2048);
+                            for (int i = 0; i < steps; ++i) {
+                                tc::tma_load_2d(a + i * 2048, &w.w_tail, &S.raw[s], f0, kk + 16 * i);
+                                tc::tma_load_2d(a + i * 2048 + 8192, &w.w_tail, &S.raw[s], f0 + 64, kk + 16 * i);
+                                tc::tma_load_2d(b + i * 2048, &w.x_tail, &S.raw[s], n0, kk + 16 * i);
+                                tc::tma_load_2d(b + i * 2048 + 8192, &w.x_tail, &S.raw[s], n0 + 64, kk + 16 * i);
+                            }
                         }
                     } else {
                         if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], 2 * (kOperand + boxes * kBox * 128));
@@ -270,25 +356,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), a_mn), b0 = tc::operand_desc(tc::smem_u32(ring) + kOperand, b_mn);
         uint32_t s = 0, phase = 0, buf = 0, buf_phase = 1;
         bool ok = true;
-        for (; ok && walk.find(w, lane); walk.t += pairs) {
+        for (; ok && walk.find(w, lane); walk.next()) {
             const Tile tl = walk.at(w);
             if (tl.kn <= 0) continue;  // zeros
             const uint32_t id = tc::idesc(FMT, a_mn, b_mn, kTile, tl.nt);
             if (!(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, kPolls))) break;
-            for (int k = 0; k < tl.kn; k += BK) {
-                if (!(ok = WEIGHTS ? tc::mbar_spin_cluster(&S.full[s], phase, err, kPolls) : tc::mbar_spin(&S.full[s], phase, err, kPolls))) break;
+            const int blocks = (tl.kn + BK - 1) / BK, early = early_at<WEIGHTS>(tl.kn);
+            uint32_t s_tail = 0, phase_tail = 0;
+            for (int j = 0; j < blocks; ++j) {
+                if (WEIGHTS && j == early && j < blocks - 1) {  // the tail's stage: at the end
+                    s_tail = s, phase_tail = phase;
+                    if (++s == (uint32_t)w.stages) s = 0, phase ^= 1;
+                }
+                const bool last = j == blocks - 1, late = WEIGHTS && last && early < blocks - 1;
+                const uint32_t at = late ? s_tail : s, ph = late ? phase_tail : phase;
+                if (!(ok = WEIGHTS ? tc::mbar_spin_cluster(&S.full[at], ph, err, kPolls) : tc::mbar_spin(&S.full[at], ph, err, kPolls))) break;
                 tc::fence_after_sync();
                 if (lead) {
-                    const uint64_t a = a0 + s * (kStage >> 4), b = b0 + s * (kStage >> 4);
+                    const uint64_t a = a0 + at * (kStage >> 4), b = b0 + at * (kStage >> 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (!WEIGHTS || k + 16 * i < tl.kn)
-                            tc::mma<true, false>(tmem + buf * kTile, a + i * astep, b + i * bstep, id, k || i);
-                    tc::mma_commit_pair(&S.empty[s]);
-                    if (k + BK >= tl.kn) tc::mma_commit_pair(&S.acc_full[buf]);
+                        if (!WEIGHTS || !last || j * BK + 16 * i < tl.kn)
+                            tc::mma<true, false>(tmem + buf * kTile, a + i * astep, b + i * bstep, id, j || i);
+                    tc::mma_commit_pair(&S.empty[at]);
+                    if (last) tc::mma_commit_pair(&S.acc_full[buf]);
                 }
                 __syncwarp();
-                if (++s == (uint32_t)w.stages) s = 0, phase ^= 1;
+                if (!late && ++s == (uint32_t)w.stages) s = 0, phase ^= 1;
             }
             buf ^= 1;
             if (buf == 0) buf_phase ^= 1;
@@ -308,11 +402,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         const uint32_t bar0 = tc::map_rank(tc::smem_u32(&S.full[0]), 0);
         uint32_t s = 0, phases = 0;
         bool ok = true;
-        for (; ok && walk.find(w, lane); walk.t += pairs) {
+        for (; ok && walk.find(w, lane); walk.next()) {
             const Tile tl = walk.at(w);
             const int blocks = (tl.kn + BK - 1) / BK, rem = tl.kn % BK;
             if (rem) {
-                const uint32_t at = (s + blocks - 1) % w.stages;
+                const uint32_t at = (s + early_at<true>(tl.kn)) % w.stages;
                 if (!(ok = tc::mbar_spin(&S.raw[at], phases >> at & 1, err, kPolls))) break;
                 phases ^= 1u << at;
                 // a row along K is 128 bytes of each of four boxes
@@ -331,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         const uint32_t release = tc::map_rank(tc::smem_u32(&S.acc_empty[0]), 0);  // of the pair's leader
         uint32_t use_acc = 0;
         bool ok = true;
-        for (; walk.find(w, lane); walk.t += pairs) {
+        for (; walk.find(w, lane); walk.next()) {
             const Tile tl = walk.at(w);
             const uint32_t buf = use_acc & 1, at = lanes + buf * kTile;
             auto let_go = [&] {
@@ -339,33 +433,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 if (lane == 0) tc::mbar_arrive_cluster(release + 8 * buf);
             };
             if constexpr (WEIGHTS) {
-                const int m = tl.f * kTile + (int)rank * kHalf + quarter * 32 + lane, c0 = half * kHalf;
-                E* row = static_cast<E*>(w.e.out) + ((int64_t)tl.g * w.features + m) * w.depth;
+                // boxes of 32 rows (lane = row) x 64 columns, swizzled as the map has
+                // it, stored by TMA, which leaves out what is past the result
+                const int m = tl.f * kTile + (int)rank * kHalf + quarter * 32;
                 if (tl.kn > 0) {
                     if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, kPolls))) break;
                     ++use_acc;
                     tc::fence_after_sync();
                 }
 #pragma unroll 1
-                for (int c = 0; c < kHalf / 32; ++c) {
-                    uint32_t r[32];
+                for (int c = 0; c < kHalf; c += 64) {
+                    uint32_t r[64];
                     if (tl.kn > 0) {
-                        tc::tmem_ld32(at + c0 + c * 32, r);
-                        tc::tmem_ld_wait(r);
-                        if (c == kHalf / 32 - 1) let_go();
+                        uint32_t q[2][32];
+                        tc::tmem_ld32(at + half * kHalf + c, q[0]);
+                        tc::tmem_ld32(at + half * kHalf + c + 32, q[1]);
+                        tc::tmem_ld_wait(q[0], q[1]);
+                        if (c + 64 == kHalf) let_go();
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) r[j] = q[j / 32][j % 32];
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = 0;
+                        for (int j = 0; j < 64; ++j) r[j] = 0;
                     }
-                    if (m < w.features)
+                    const int col = tl.n0 + half * kHalf + c;
+                    if (m >= w.features || col >= w.depth) continue;
+                    uint8_t* patch = patches + ew * patch_bytes(KIND);
+                    if (lane == 0) tc::tma_store_read<0>();
+                    __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int col = tl.n0 + c0 + c * 32 + 8 * j;
-                            float v[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
-                            if (col < w.depth) store8(row + col, true, 8, v);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        uint4 v;
+                        v.x = Elem<E>::pack(__uint_as_float(r[8 * j]), __uint_as_float(r[8 * j + 1]));
+                        v.y = Elem<E>::pack(__uint_as_float(r[8 * j + 2]), __uint_as_float(r[8 * j + 3]));
+                        v.z = Elem<E>::pack(__uint_as_float(r[8 * j + 4]), __uint_as_float(r[8 * j + 5]));
+                        v.w = Elem<E>::pack(__uint_as_float(r[8 * j + 6]), __uint_as_float(r[8 * j + 7]));
+                        *reinterpret_cast<uint4*>(patch + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::tma_store_3d(&w.out, patch, col, m, tl.g);
                 }
             } else {
                 Epi e = w.e;
@@ -398,7 +505,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                                 float v[8], u[8];
                                 patch_get(mine + turn, rr, c8, v);
                                 patch_get(mine + turn + 4096, rr, c8, u);
-                                epi_store<E, EPI_GATED, decltype(act)::value>(e, tl.n0 + c + rr, col, v, EpiIn{}, v, u);
+                                const int row = tl.n0 + c + rr;
+                                if (row >= e.rows || col >= e.cols) continue;
+                                if (e.keep) {
+                                    float* k = static_cast<float*>(e.keep) + row * e.ld_keep + col;
+                                    store8_f32(k, true, 8, v);
+                                    store8_f32(k + e.cols, true, 8, u);
+                                }
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) v[j] = act_fwd(decltype(act)::value, v[j]) * u[j];
+                                store8(static_cast<E*>(e.out) + row * e.ld_out + col, true, 8, v);
                             }
                         });
                     }
@@ -408,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                     uint8_t* patch = patches + ew * patch_bytes(KIND);
 #pragma unroll 1
                     for (int c = half * 32; c < live; c += 64) {
-                        Ahead<E, EPI> x;
+                        Before<E, KIND> x;
                         x.load(e, lane, tl.n0 + c, f);
                         uint32_t r[32];
                         tc::tmem_ld32(at + c, r);
@@ -417,12 +533,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                         __syncwarp();  // the patch's last readers are done
                         patch_put_t(patch, lane, r);
                         __syncwarp();
-                        patch_out<E, EPI>(e, patch, lane, tl.n0 + c, f, x);
+                        x.out(e, patch, lane, tl.n0 + c, f);
                     }
                 }
             }
         }
     }
+    if (WEIGHTS && warp >= 4 && lane == 0) tc::tma_store_done();
     // neither CTA leaves, and no TMEM is freed, while the other may still use it
     __syncwarp();
     tc::fence_before_sync();
@@ -469,8 +586,13 @@ cudaError_t launch(const Grouped& p, uint32_t* err, cudaStream_t st) {
     constexpr int NF = KIND == GROUP_GATED ? kHalf : kTile;
     Work w = {};
     if (WEIGHTS) {
-        if (!encode_operand(&w.w, p.w, p.ld_w, p.features, p.rows, true, false, 0) ||
-            !encode_operand(&w.x, p.x, p.ld_x, p.depth, p.rows, true, false, 0))
+        const uint64_t wd[2] = {(uint64_t)p.features, (uint64_t)p.rows}, ws[1] = {2 * (uint64_t)p.ld_w};
+        const uint64_t xd[2] = {(uint64_t)p.depth, (uint64_t)p.rows}, xs[1] = {2 * (uint64_t)p.ld_x};
+        const uint64_t od[3] = {(uint64_t)p.depth, (uint64_t)p.features, (uint64_t)p.groups}, os[2] = {2 * od[0], 2 * od[0] * od[1]};
+        const uint32_t whole[2] = {64, 64}, tail[2] = {64, 16}, out[3] = {64, 32, 1};
+        if (!encode_boxes(&w.w, p.w, 2, wd, ws, whole, false) || !encode_boxes(&w.x, p.x, 2, xd, xs, whole, false) ||
+            !encode_boxes(&w.w_tail, p.w, 2, wd, ws, tail, false) || !encode_boxes(&w.x_tail, p.x, 2, xd, xs, tail, false) ||
+            !encode_boxes(&w.out, p.e.out, 3, od, os, out, false))
             return cudaErrorInvalidValue;
     } else {
         const uint64_t lines = (uint64_t)p.features * (KIND == GROUP_GATED ? 2 : 1), k = p.depth;

@@ -577,7 +577,7 @@ PyObject* grouped_ffn(PyObject* self, Args args, Py_ssize_t n) {
     const size_t bytes = pe_grouped_ffn_workspace((int32_t)x.d0, (int32_t)inter);
     const at::Tensor y = empty(x.dev, x.dt, x.d0, x.d1), ws = empty(x.dev, kU8, (int64_t)bytes);
     at::Tensor gu;
-    if (save) gu = empty(x.dev, x.dt, x.d0, 2 * inter);
+    if (save) gu = empty(x.dev, kF32, x.d0, 2 * inter);
     call([&] {
         return pe_grouped_ffn(x.p, x.s0, w13.p, w2.p, (const int32_t*)off.p, ptr(y), ptr(gu), act, ptr(ws), bytes, (int32_t)x.d0,
                               (int32_t)groups, (int32_t)x.d1, (int32_t)inter, elem, current(x.dev));
@@ -591,7 +591,7 @@ PyObject* grouped_ffn_backward(PyObject* self, Args args, Py_ssize_t n) {
     const int act = act_of(args[6]), elem = elem_of(x.dt, "x");
     const auto [g, i] = experts_of(x, w13, w2);
     const int64_t groups = g, inter = i;
-    const Ten dy = rows_of(args[0], "dy", x.dt, x.d0, x.d1), gu = whole_of(args[4], "gu", x.dt, x.d0, 2 * inter);
+    const Ten dy = rows_of(args[0], "dy", x.dt, x.d0, x.d1), gu = whole_of(args[4], "gu", kF32, x.d0, 2 * inter);
     const Ten off = offsets_of(args[5], groups);
     together(x, {&dy, &w13, &w2, &gu, &off});
     if (away(args[7], x.dev)) return go_there(self, "grouped_ffn_backward", x.dev, args, n);

@@ -217,7 +217,8 @@ def grouped_linear_backward(dy, x, weight, offsets, *, stream=None):
 
 def grouped_ffn(x, w13, w2, offsets, act: str = "silu", *, save: bool = False, stream=None):
     """``gated_ffn`` of each group's rows with its own weights: w13 [groups, 2 I, H],
-    w2 [groups, H, I].  ``save`` returns (out, gu) for ``grouped_ffn_backward``."""
+    w2 [groups, H, I].  ``save`` returns (out, gu) with the fp32 [rows, 2 I] gate and
+    up products for ``grouped_ffn_backward``."""
     return (_native or _c()).grouped_ffn(x, w13, w2, offsets, act, save, stream)
 
 

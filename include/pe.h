@@ -540,8 +540,9 @@ pe_status pe_grouped_linear_backward(const void* dy, int64_t dy_stride, const vo
                                      int32_t elem, void* stream);
 
 /* pe_gated_ffn with the weights of each group: w13 [groups, 2 intermediate,
- * hidden], w2 [groups, hidden, intermediate]; no residual.  keep: [rows,
- * 2 intermediate] or NULL.  Rows in no group stay as they were.
+ * hidden], w2 [groups, hidden, intermediate]; no residual.  keep: fp32 [rows,
+ * 2 intermediate] x gate^T and x up^T, or NULL.  Rows in no group stay as they
+ * were.
  * workspace: pe_grouped_ffn_workspace(rows, intermediate) bytes. */
 size_t pe_grouped_ffn_workspace(int32_t rows, int32_t intermediate);
 pe_status pe_grouped_ffn(const void* x, int64_t x_stride, const void* w13, const void* w2, const int32_t* offsets,

@@ -115,8 +115,10 @@ def grouped_linear_backward(dy, x, w, offsets, dt):
 
 
 def grouped_ffn(x, w13, w2, offsets, a, dt):
-    parts = [R.gated_ffn(x[s], w13[g], w2[g], a, None, dt) for g, s in enumerate(_groups(offsets))]
-    return {n: _cat([p[n] for p in parts]) for n in ("y", "gu")}
+    """gu is kept in fp32."""
+    gs = list(enumerate(_groups(offsets)))
+    return {"y": _cat([R.gated_ffn(x[s], w13[g], w2[g], a, None, dt)["y"] for g, s in gs]),
+            "gu": _cat([R.mm(q(x[s]), q(w13[g])) for g, s in gs]).rounded(torch.float32)}
 
 
 def grouped_ffn_backward(dy, x, w13, w2, gu, offsets, a, dt):

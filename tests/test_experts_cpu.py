@@ -26,7 +26,7 @@ def t(*shape, dt=BF):
 
 
 X, LG, IDS, W = t(4, 64), t(4, 16, dt=F32), t(4, 2, dt=I32), t(4, 2, dt=F32)
-GW, OFF, W13, W2, GU = t(3, 24, 64), t(4, dt=I32), t(3, 32, 64), t(3, 64, 16), t(4, 32)
+GW, OFF, W13, W2, GU = t(3, 24, 64), t(4, dt=I32), t(3, 32, 64), t(3, 64, 16), t(4, 32, dt=F32)
 C, S4, SM, SN, TS = t(24, 32, dt=U8), t(24, 1, dt=HF), t(24, 2, dt=U8), t(24, 4, dt=F8), t(1, dt=F32)
 
 
@@ -62,7 +62,7 @@ C, S4, SM, SN, TS = t(24, 32, dt=U8), t(24, 1, dt=HF), t(24, 2, dt=U8), t(24, 4,
     (lambda: dense.grouped_ffn(X, W13, t(3, 56, 16), OFF), "w2: want"),
     (lambda: dense.grouped_ffn(X, W13[:2], W2, OFF), "w13: want"),
     (lambda: dense.grouped_ffn(X, W13, W2, OFF, "tanh"), "unknown activation"),
-    (lambda: dense.grouped_ffn_backward(X, X, W13, W2, t(4, 16), OFF), "gu: want"),
+    (lambda: dense.grouped_ffn_backward(X, X, W13, W2, t(4, 32), OFF), "gu: want"),
     (lambda: dense.linear_w4(X, C, S4, "int8"), "unknown format 'int8'"),
     (lambda: dense.linear_w4(t(4, 48), t(24, 24, dt=U8), S4, "int4"), "multiple of 32"),
     (lambda: dense.linear_w4(X, C[:, :16], S4, "int4"), "codes: want contiguous Byte [24, 32]"),
