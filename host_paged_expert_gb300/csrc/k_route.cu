@@ -8,8 +8,8 @@
 //
 // Places: an expert is chosen at most once per token, so 32 tokens' choices of
 // it are the bits of one word, and an entry's rank among its expert's is a
-// popcount of the bits below its token's.  A block takes a chunk of tokens,
-// 32 at a time, and leaves ranks inside the chunk and the chunk's counts; a
+// popcount of the bits below its token's.  A block takes a chunk of tokens, kTokens
+// at a time, and leaves ranks inside the chunk and the chunk's counts; a
 // second launch adds up the counts of the chunks before each one and of all
 // experts before.  Up to kAloneTokens one block does it all in one launch.
 // Nothing depends on the order of atomics: the bits are OR-ed.
@@ -20,7 +20,8 @@ namespace pe {
 namespace dense {
 namespace {
 
-constexpr int kThreads = 1024, kTokens = 32;  // a warp per token of a batch
+constexpr int kThreads = 1024;                  // a warp per token
+constexpr int kWords = 4, kTokens = 32 * kWords;  // tokens of a batch
 constexpr int kAloneTokens = 128;
 constexpr int kMostChunks = 152;
 
@@ -35,29 +36,75 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
+// A token's logits on their way.  vec: rows of whole, aligned fours.
 template <int EPL>
-__device__ __forceinline__ void pick(const float* row, int experts, int k, int lane, int& id, float& w) {
-    uint32_t key[EPL];
+__device__ __forceinline__ void fetch(const float* row, int experts, bool vec, int lane, float (&v)[EPL]) {
+    if (EPL % 4 == 0 && vec) {
 #pragma unroll
-    for (int q = 0; q < EPL; ++q) {
-        const int e = lane * EPL + q;
-        key[q] = e < experts ? key_of(row[e]) : 0;
+        for (int q = 0; q < EPL; q += 4) {
+            const int e = lane * EPL + q;
+            const float4 f = e < experts ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[q] = f.x, v[(q + 1) % EPL] = f.y, v[(q + 2) % EPL] = f.z, v[(q + 3) % EPL] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < EPL; ++q) v[q] = lane * EPL + q < experts ? row[lane * EPL + q] : 0.f;
+    }
+}
+
+// SORTED: a lane's keys are put in order first (by neighbours, so that equal
+// ones stay in the order of their experts), and a pick takes its head away;
+// else a pick looks for the largest left.  Sorting pays up to eight keys: of
+// 16384 tokens x 128 experts 14 us without, 7 with it.
+template <int EPL>
+__device__ __forceinline__ void pick(const float (&v0)[EPL], int experts, int k, int lane, int& id, float& w) {
+    constexpr bool SORTED = EPL <= 8;
+    uint32_t key[EPL], at = 0;  // SORTED: at, four bits each, the places of the keys
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) key[q] = lane * EPL + q < experts ? key_of(v0[q]) : 0;
+    if (SORTED) {
+        uint32_t from[EPL];
+#pragma unroll
+        for (int q = 0; q < EPL; ++q) from[q] = q;
+#pragma unroll
+        for (int n = EPL - 1; n > 0; --n)
+#pragma unroll
+            for (int q = 0; q < n; ++q) {
+                const bool swap = key[q] < key[q + 1];
+                const uint32_t f = from[q], hi = max(key[q], key[q + 1]);
+                key[q + 1] = min(key[q], key[q + 1]);
+                key[q] = hi;
+                from[q] = swap ? from[q + 1] : f;
+                from[q + 1] = swap ? f : from[q + 1];
+            }
+#pragma unroll
+        for (int q = 0; q < EPL; ++q) at |= from[q] << (4 * q);
     }
     uint32_t mine = 0;  // key of this lane's pick
     id = -1;
     for (int j = 0; j < k; ++j) {
         uint32_t best = key[0];
-        int at = 0;
+        if (!SORTED) {
+            at = 0;
 #pragma unroll
-        for (int q = 1; q < EPL; ++q)
-            if (key[q] > best) best = key[q], at = q;
+            for (int q = 1; q < EPL; ++q)
+                if (key[q] > best) best = key[q], at = q;
+        }
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         const int owner = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-        const int e = __shfl_sync(0xffffffffu, lane * EPL + at, owner);
-        if (lane == owner)
+        const int e = owner * EPL + (int)(__shfl_sync(0xffffffffu, at, owner) & (SORTED ? 15u : 31u));
+        if (lane == owner) {
+            if (SORTED) {
 #pragma unroll
-            for (int q = 0; q < EPL; ++q)
-                if (q == at) key[q] = 0;
+                for (int q = 0; q + 1 < EPL; ++q) key[q] = key[q + 1];
+                key[EPL - 1] = 0;
+                at >>= 4;
+            } else {
+#pragma unroll
+                for (int q = 0; q < EPL; ++q)
+                    if (q == (int)at) key[q] = 0;
+            }
+        }
         if (lane == j) id = e, mine = top;
     }
     // the softmax over the chosen; infinities that lead share the weight
@@ -95,33 +142,61 @@ __device__ __forceinline__ int scan_block(int v, int* part, int& total) {
 
 // ALONE: the one block of its launch, which finishes the places and offsets.
 template <int EPL, bool ALONE>
-__global__ void __launch_bounds__(kThreads) choose_kernel(const RouteArgs a, int chunk_tokens) {
-    __shared__ uint32_t bits[kMaxGroups];
+__global__ void __launch_bounds__(kThreads) choose_kernel(const RouteArgs a, int chunk_tokens, bool vec) {
+    __shared__ uint32_t bits[kMaxGroups][kWords];  // bit t of word w: token 32 w + t of the batch chose this expert
     __shared__ int run[kMaxGroups], part[32];
+    __shared__ uint16_t chosen[kTokens / 32][32][kMostTopK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) bits[e] = run[e] = 0;
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+        run[e] = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) bits[e][w] = 0;
+    }
     pdl_wait();
     pdl_trigger();
     __syncthreads();
     const int t0 = blockIdx.x * chunk_tokens, t1 = min(a.tokens - t0, chunk_tokens) + t0;
+    constexpr bool AHEAD = EPL <= 16;  // registers for the next token's logits
     for (int tb = t0; tb < t1; tb += kTokens) {
-        const int t = tb + warp;
-        int id = -1;
-        float w;
-        if (t < t1) {
-            pick<EPL>(a.logits + t * a.ld, a.experts, a.k, lane, id, w);
+        // a warp's tokens of the batch: one of each word
+        float next[EPL];
+        if (AHEAD && tb + warp < t1) fetch<EPL>(a.logits + (tb + warp) * a.ld, a.experts, vec, lane, next);
+#pragma unroll 1
+        for (int w = 0; w < kWords; ++w) {
+            const int t = tb + 32 * w + warp;
+            if (t >= t1) break;
+            float v[EPL], weight;
+            int id;
+            if (AHEAD) {
+#pragma unroll
+                for (int q = 0; q < EPL; ++q) v[q] = next[q];
+                if (w + 1 < kWords && t1 - t > 32) fetch<EPL>(a.logits + (t + 32) * a.ld, a.experts, vec, lane, next);
+            } else {
+                fetch<EPL>(a.logits + t * a.ld, a.experts, vec, lane, v);
+            }
+            pick<EPL>(v, a.experts, a.k, lane, id, weight);
             if (lane < a.k) {
                 a.ids[(int64_t)t * a.k + lane] = id;
-                a.weights[(int64_t)t * a.k + lane] = w;
-                atomicOr(&bits[id], 1u << warp);
+                a.weights[(int64_t)t * a.k + lane] = weight;
+                chosen[w][warp][lane] = (uint16_t)id;
+                atomicOr(&bits[id][w], 1u << warp);
             }
         }
         __syncthreads();
-        if (id >= 0) a.place[(int64_t)t * a.k + lane] = run[id] + __popc(bits[id] & ((1u << warp) - 1));
+        // ranks: entries of the batch in turn, whole lines at a time
+        const int entries = min(kTokens, t1 - tb) * a.k;
+        for (int i = threadIdx.x; i < entries; i += kThreads) {
+            const int t = i / a.k, id = chosen[t / 32][t % 32][i - t * a.k];
+            int rank = run[id] + __popc(bits[id][t / 32] & ((1u << t % 32) - 1));
+            for (int w = 0; w < t / 32; ++w) rank += __popc(bits[id][w]);
+            a.place[(int64_t)tb * a.k + i] = rank;
+        }
         __syncthreads();
         for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-            run[e] += __popc(bits[e]);
-            bits[e] = 0;
+            int n = run[e];
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) n += __popc(bits[e][w]), bits[e][w] = 0;
+            run[e] = n;
         }
         __syncthreads();
     }
@@ -144,16 +219,25 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const RouteArgs a, int 
     for (int e = threadIdx.x; e < a.experts; e += kThreads) before[e] = all[e] = 0;
     pdl_wait();
     pdl_trigger();
+    const int t0 = blockIdx.x * chunk_tokens, t1 = min(a.tokens - t0, chunk_tokens) + t0;
+    const int64_t first_entry = (int64_t)t0 * a.k + threadIdx.x, last_entry = (int64_t)t1 * a.k;
+    int id0 = 0, place0 = 0;  // asked for ahead of the sums
+    if (first_entry < last_entry) id0 = a.ids[first_entry], place0 = a.place[first_entry];
     __syncthreads();
     // a group of threads per expert's share of the chunks
     const int lanes = min(kThreads, (a.experts + 31) / 32 * 32), shares = kThreads / lanes;
     const int share = threadIdx.x / lanes, e0 = threadIdx.x % lanes;
     if (share < shares && e0 < a.experts) {
         int b = 0, s = 0;
-        for (int c = share; c < (int)gridDim.x; c += shares) {
-            const int n = a.counts[(int64_t)c * a.experts + e0];
-            s += n;
-            if (c < (int)blockIdx.x) b += n;
+        for (int c0 = share; c0 < (int)gridDim.x; c0 += 8 * shares) {
+            int n[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) n[u] = c0 + u * shares < (int)gridDim.x ? a.counts[(int64_t)(c0 + u * shares) * a.experts + e0] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                s += n[u];
+                if (c0 + u * shares < (int)blockIdx.x) b += n[u];
+            }
         }
         atomicAdd(&before[e0], b);
         atomicAdd(&all[e0], s);
@@ -167,8 +251,8 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const RouteArgs a, int 
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.experts] = total;
     __syncthreads();
-    const int t0 = blockIdx.x * chunk_tokens, t1 = min(a.tokens - t0, chunk_tokens) + t0;
-    for (int64_t i = (int64_t)t0 * a.k + threadIdx.x; i < (int64_t)t1 * a.k; i += kThreads) a.place[i] += before[a.ids[i]];
+    if (first_entry < last_entry) a.place[first_entry] = place0 + before[id0];
+    for (int64_t i = first_entry + kThreads; i < last_entry; i += kThreads) a.place[i] += before[a.ids[i]];
 }
 
 // dlogits[t, ids[i]] = w_i (dw_i - sum_j w_j dw_j), zero elsewhere; an expert
@@ -210,17 +294,18 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwdArgs a) {
     if (lane < a.k && first && id >= 0 && id < a.experts) row[id] = sum;
 }
 
-// Tokens of a chunk: whole batches of 32, in at most kMostChunks chunks.
+// Tokens of a chunk: whole words of 32, in at most kMostChunks chunks.
 int chunk_of(int tokens) {
-    const int batches = (tokens - 1) / kTokens + 1;
-    return ((batches - 1) / kMostChunks + 1) * kTokens;
+    const int words = (tokens - 1) / 32 + 1;
+    return ((words - 1) / kMostChunks + 1) * 32;
 }
 
 template <int EPL>
 cudaError_t choose(const RouteArgs& a, cudaStream_t st) {
-    if (a.tokens <= kAloneTokens) return launch_pdl(choose_kernel<EPL, true>, dim3(1), dim3(kThreads), 0, st, a, a.tokens);
+    const bool vec = a.experts % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+    if (a.tokens <= kAloneTokens) return launch_pdl(choose_kernel<EPL, true>, dim3(1), dim3(kThreads), 0, st, a, a.tokens, vec);
     const int chunks = route_chunks(a.tokens);
-    if (cudaError_t e = launch_pdl(choose_kernel<EPL, false>, dim3(chunks), dim3(kThreads), 0, st, a, chunk_of(a.tokens))) return e;
+    if (cudaError_t e = launch_pdl(choose_kernel<EPL, false>, dim3(chunks), dim3(kThreads), 0, st, a, chunk_of(a.tokens), vec)) return e;
     return launch_pdl(place_kernel, dim3(chunks), dim3(kThreads), 0, st, a, chunk_of(a.tokens));
 }
 
