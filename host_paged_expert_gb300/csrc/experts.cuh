@@ -88,9 +88,11 @@ struct W4Args {
     int M, N, K, fmt;
     Epi e;
 };
-// Rows that the streaming kernel takes; above, the weights are unpacked first.
-constexpr int kW4Rows = 64;
+// Rows that the kernel streaming into registers takes, and the one that decodes
+// into shared memory; above, the weights are unpacked first.
+constexpr int kW4Stream = 16, kW4Rows = 128;
 cudaError_t launch_w4(const W4Args& a, int elem, cudaStream_t st);
+cudaError_t launch_w4_tc(const W4Args& a, int elem, uint32_t* err, cudaStream_t st);
 // w [N, K] of the element type = codes times scales
 cudaError_t launch_w4_unpack(const W4Args& a, void* w, int elem, cudaStream_t st);
 

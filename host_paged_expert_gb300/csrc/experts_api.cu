@@ -384,9 +384,10 @@ extern "C" pe_status pe_linear_four_bit(const void* x, int64_t x_stride, const v
     a.e.bias = bias;
     a.e.res = residual;
     a.e.ld_res = residual_stride;
-    if (rows <= kW4Rows) return done(launch_w4(a, elem, st));
+    if (rows <= kW4Stream) return done(launch_w4(a, elem, st));
     uint32_t* err = nullptr;
     cudaError_t e = error_word(&err);
+    if (rows <= kW4Rows) return done(e ? e : launch_w4_tc(a, elem, err, st));
     if (!e) e = launch_w4_unpack(a, workspace, elem, st);
     if (!e) {
         Product p = {};

@@ -28,6 +28,7 @@
 // terms), so no more than 512 terms go into one accumulator while TMEM has
 // room, and those are added in registers.
 #include "dense.cuh"
+#include "dense_cluster.cuh"
 #include "dense_tc.cuh"
 #include "pe_device.cuh"
 
@@ -37,7 +38,6 @@ namespace dense {
 namespace {
 
 constexpr int kThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..7 epilogue; all of them add up
-constexpr int kRows = 128;     // weight rows of a tile
 constexpr int kP = kRows * 128;  // bytes of their stage
 constexpr int kMaxStages = 8;
 
@@ -58,69 +58,6 @@ struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[8], acc_empty[8], drain;
     uint32_t tmem;
 };
-
-// Adds up the cluster's partials of units of eight columns in a row, in rank
-// order, and applies the epilogue.  Each thread asks for all the parts of
-// several units before it adds the first: the round trip to another SM's
-// shared memory is paid once.
-// split: CTAs of the cluster, at most SPLIT.
-template <typename E, int KIND, int SPLIT>
-__device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt, int split, int rank, int t0, int f0) {
-    constexpr int NF = KIND == EPI_GATED ? kRows / 2 : kRows, U = NF / 8, G = KIND == EPI_GATED ? 2 : 1;
-    constexpr int BATCH = 4 / (SPLIT * G) > 1 ? 4 / (SPLIT * G) : 1;
-    // each rank takes whole rows, as many as the others
-    const int rows = min(nt, e.rows - t0), mine = (rows + split - 1) / split, r0 = rank * mine;
-    const int total = min(mine, rows - r0) * U;
-    uint32_t from[SPLIT];
-#pragma unroll
-    for (int r = 0; r < SPLIT; ++r) from[r] = tc::map_rank(tc::smem_u32(ring), r < split ? r : 0);
-    // the stride between a thread's units is a multiple of U: its columns stay the same
-    const int u0 = (int)threadIdx.x, col = f0 + (u0 % U) * 8;
-    float bias[8];
-    epi_cols<E, KIND>(e, col, bias);
-    for (int ub = u0; ub < total; ub += kThreads * BATCH) {
-        float v[BATCH][G][8];
-        EpiIn in[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int u = ub + i * kThreads, t = r0 + u / U;
-            const uint32_t at = (uint32_t)(t * kRows + (u0 % U) * 8) * 4;
-            in[i] = epi_load<E, KIND>(e, u < total ? t0 + t : e.rows, col);
-            if (u >= total) continue;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float4 a[SPLIT][2];
-#pragma unroll
-                for (int r = 0; r < SPLIT; ++r)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (SPLIT <= 2 || r < split) a[r][h] = tc::ld_cluster_f4(from[r] + at + g * NF * 4 + h * 16);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][g][j] = 0.f;
-#pragma unroll
-                for (int r = 0; r < SPLIT; ++r)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (SPLIT > 2 && r >= split) continue;
-                        float* d = v[i][g] + 4 * h;
-                        d[0] += a[r][h].x, d[1] += a[r][h].y, d[2] += a[r][h].z, d[3] += a[r][h].w;
-                    }
-            }
-        }
-        with_act(e.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const int u = ub + i * kThreads;
-                if (u < total) {
-                    if (epi_light<KIND>(e))
-                        epi_store_light<E, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0]);
-                    else
-                        epi_store<E, KIND, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0], v[i][G - 1]);
-                }
-            }
-        });
-    }
-}
 
 // LIMITED: the waits' limits are the launch's.
 template <typename E, int KIND, bool FP8, bool LIMITED>
@@ -347,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ---- the tile's sum over the cluster, and the epilogue
-    if (q.split == 1) reduce<E, KIND, 1>(p.e, ring, q.nt, 1, rank, t0, f0);
-    else if (q.split == 2) reduce<E, KIND, 2>(p.e, ring, q.nt, 2, rank, t0, f0);
-    else if (q.split <= 4) reduce<E, KIND, 4>(p.e, ring, q.nt, q.split, rank, t0, f0);
-    else reduce<E, KIND, 8>(p.e, ring, q.nt, q.split, rank, t0, f0);
+    if (q.split == 1) reduce<E, KIND, 1, kThreads>(p.e, ring, q.nt, 1, rank, t0, f0);
+    else if (q.split == 2) reduce<E, KIND, 2, kThreads>(p.e, ring, q.nt, 2, rank, t0, f0);
+    else if (q.split <= 4) reduce<E, KIND, 4, kThreads>(p.e, ring, q.nt, q.split, rank, t0, f0);
+    else reduce<E, KIND, 8, kThreads>(p.e, ring, q.nt, q.split, rank, t0, f0);
     // no CTA leaves while another may read its partial
     if (q.split > 1) {
         tc::cluster_arrive_relaxed();

@@ -564,10 +564,10 @@ pe_status pe_grouped_ffn_backward(const void* dy, int64_t dy_stride, const void*
  *   scales: int4: fp16 [out, ceil(in/128)], W = (code - 8) * scale; MXFP4: E8M0
  *     [out, in/32]; NVFP4: E4M3 [out, in/16], times tensor_scale[0] (device; NULL
  *     for the other formats).
- * Up to 64 rows the weights are streamed and used unrounded (with fp16, MXFP4
- * scales above 2^16 count as 2^16 and are lost below 2^-23; with bf16 they are
- * cut at 2^120); above, they are unpacked to elem in the workspace first:
- * int4's and NVFP4's products with their scales are rounded there.
+ * Up to 128 rows the weights are used unrounded (with fp16, MXFP4 scales above
+ * 2^15 count as 2^15 and are lost below 2^-24); above, they are unpacked to elem
+ * in the workspace first: int4's and NVFP4's products with their scales are
+ * rounded there, and a weight beyond fp16's range is infinite.
  * in: a multiple of 32.
  * workspace: pe_linear_four_bit_workspace(rows, in, out) bytes. */
 size_t pe_linear_four_bit_workspace(int32_t rows, int32_t in_features, int32_t out_features);

@@ -176,8 +176,8 @@ def test_c_calls_refuse(L, name, at, value, status):
 
 def test_workspaces(L):
     up = lambda n: -(-n // 256) * 256  # noqa: E731
-    assert L.pe_linear_four_bit_workspace(64, 4096, 2048) == 0
-    assert L.pe_linear_four_bit_workspace(65, 4096, 2048) == up(2 * 4096 * 2048)
+    assert L.pe_linear_four_bit_workspace(128, 4096, 2048) == 0
+    assert L.pe_linear_four_bit_workspace(129, 4096, 2048) == up(2 * 4096 * 2048)
     assert L.pe_grouped_ffn_workspace(100, 40) == up(2 * 100 * 40)
     assert L.pe_grouped_ffn_backward_workspace(100, 40) == up(4 * 100 * 40) + up(2 * 100 * 40)
     # never more chunks of tokens than a launch has blocks for
