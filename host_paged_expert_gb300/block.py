@@ -6,6 +6,8 @@ residual's addition, the router, the routed experts (paged) next to a shared
 expert, and the next layer's input norm with its 8-bit form in front of a
 block-FP8 projection.  ``DenseBlock`` is the layer of the same stack that has
 no routing (norm, gated feed-forward, residual), with its backward pass.
+``ExpertBlock`` is the layer with routing whose experts are resident: it trains
+what ``PagedBlock`` serves.
 """
 
 from __future__ import annotations
@@ -59,3 +61,35 @@ class DenseBlock:
         # dy also reaches x by the residual
         dx, dnorm = dense.rms_norm_backward(dn, n.sum, self.norm, n.rstd, dsum=dy)
         return dx, {"norm": dnorm, "w13": dw13, "w2": dw2}
+
+
+class ExpertBlock:
+    """x + the weighted sum of its tokens' experts (rms_norm(x)): a layer whose
+    routed experts are resident, for training.
+
+    bf16 or fp16: ``norm`` [H], ``router`` [E, H], ``w13`` [E, 2 I, H], ``w2``
+    [E, H, I].  The router's logits are fp32; its choice has no gradient, its
+    weights do."""
+
+    def __init__(self, *, norm, router, w13, w2, top_k: int, act: str = "silu", eps: float = 1e-6):
+        self.norm, self.router, self.w13, self.w2, self.top_k, self.act, self.eps = norm, router, w13, w2, top_k, act, eps
+
+    def forward(self, x):
+        """(out, what backward needs).  Kernel launches only: capturable."""
+        n = dense.rms_norm(x, self.norm, eps=self.eps, save=True)
+        r = dense.route(dense.linear(n.y, self.router, out_dtype=torch.float32), self.top_k)
+        rows = dense.expand_rows(n.y, r.place)
+        y, gu = dense.grouped_ffn(rows, self.w13, self.w2, r.offsets, self.act, save=True)
+        return dense.combine_rows(y, r.place, r.weights, x), (n, r, rows, gu, y)
+
+    def backward(self, dout, saved):
+        """(dx, {"norm": , "router": , "w13": , "w2": } gradients)"""
+        n, r, rows, gu, y = saved
+        dy, dweights = dense.combine_rows_backward(dout, y, r.place, r.weights)
+        drows, dw13, dw2 = dense.grouped_ffn_backward(dy, rows, self.w13, self.w2, gu, r.offsets, self.act)
+        # the logits' gradient in the type that the product's MMA takes
+        dlogits = dense.route_backward(dweights, r.weights, r.ids, self.router.shape[0]).to(n.y.dtype)
+        dn, drouter, _ = dense.linear_backward(dlogits, n.y, self.router)
+        dn = dense.combine_rows(drows, r.place, residual=dn)
+        dx, dnorm = dense.rms_norm_backward(dn, n.sum, self.norm, n.rstd, dsum=dout)
+        return dx, {"norm": dnorm, "router": drouter, "w13": dw13, "w2": dw2}

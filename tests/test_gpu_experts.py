@@ -512,3 +512,122 @@ def test_captured(D):
     torch.cuda.synchronize()
     for _, got in graphs:
         assert all(same(a, b) for a, b in zip(ref, got))
+
+
+# ---- the layer
+
+
+def _block(seed=0, H=128, E=12, I=72, k=3, dt=BF):
+    from host_paged_expert_gb300.block import ExpertBlock
+
+    return ExpertBlock(norm=1 + rand(H, seed=seed, scale=0.1, dt=dt), router=rand(E, H, seed=seed + 1, scale=H**-0.5, dt=dt),
+                       w13=rand(E, 2 * I, H, seed=seed + 2, scale=H**-0.5, dt=dt), w2=rand(E, H, I, seed=seed + 3, scale=I**-0.5, dt=dt), top_k=k)
+
+
+@pytest.mark.parametrize("T", [1, 7, 300])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_expert_block(D, T, dt):
+    """Each stage of ExpertBlock against the formulas, from what the stage before
+    it left."""
+    b = _block(dt=dt)
+    x, dout = rand(T, 128, seed=9, dt=dt), rand(T, 128, seed=10, dt=dt)
+    out, saved = b.forward(x)
+    n, r, rows, gu, y = saved
+    logits = D.linear(n.y, b.router, out_dtype=F32)
+    ids, w, offsets, place = X.route(logits, 3)
+    assert torch.equal(r.ids, ids) and torch.equal(r.offsets, offsets) and torch.equal(r.place, place)
+    assert same(rows[place.flatten().long()], n.y.repeat_interleave(3, 0))
+    want = X.grouped_ffn(rows, b.w13, b.w2, offsets, "silu", dt)
+    R.check(y, want["y"], "y")
+    R.check(out, X.combine(y, place, r.weights, x, dt), "out")
+    dx, g = b.backward(dout, saved)
+    dy, dw = D.combine_rows_backward(dout, y, place, r.weights)
+    f = X.grouped_ffn_backward(dy, rows, b.w13, b.w2, gu, offsets, "silu", dt)
+    R.check(g["w13"], f["dw13"], "dw13")
+    R.check(g["w2"], f["dw2"], "dw2")
+    dl = D.route_backward(dw, r.weights, r.ids, 12).to(dt)
+    lb = R.linear_backward(dl, n.y, b.router, None, "none", dt)
+    R.check(g["router"], lb["dw"], "drouter")
+    dn = D.combine_rows(D.grouped_ffn_backward(dy, rows, b.w13, b.w2, gu, offsets)[0], place, residual=D.linear_backward(dl, n.y, b.router)[0])
+    nb = R.rms_norm_backward(dn, x, b.norm, n.rstd, dout, dt)
+    R.check(dx, nb["dx"], "dx")
+    R.check(g["norm"], nb["dw"], "dnorm")
+
+
+def test_expert_block_against_differences(D):
+    """The whole layer's gradients along random directions, against central
+    differences of the layer's formula in 64 bits with the same choice of
+    experts (the choice has no gradient)."""
+    T, H, E, I, k = 40, 128, 12, 72, 3
+    b = _block(dt=HF)
+    x, c = rand(T, H, seed=9, dt=HF), rand(T, H, seed=10, dt=HF)
+    out, saved = b.forward(x)
+    ids = saved[1].ids.long()
+    dx, g = b.backward(c, saved)
+
+    def loss(x, norm, router, w13, w2):
+        n = x * (x.square().mean(1, keepdim=True) + b.eps).rsqrt() * norm
+        w = torch.softmax((n @ router.t()).gather(1, ids), 1)
+        z = torch.einsum("th,tkih->tki", n, w13[ids])
+        h = R.phi("silu", z[:, :, :I])[0] * z[:, :, I:]
+        return ((x + (torch.einsum("tki,tkhi->tkh", h, w2[ids]) * w[:, :, None]).sum(1)) * c.double()).sum()
+
+    at = [t.double() for t in (x, b.norm, b.router, b.w13, b.w2)]
+    for which, got in enumerate((dx, g["norm"], g["router"], g["w13"], g["w2"])):
+        u = torch.randn(got.shape, generator=gen(which), device="cuda", dtype=torch.float64)
+        lo, hi = [[t + s * u if j == which else t for j, t in enumerate(at)] for s in (-1e-5, 1e-5)]
+        want = (loss(*hi) - loss(*lo)) / 2e-5
+        # independent roundings to fp16 of the activations and gradients on the way, a
+        # dozen of half a step each, and as much again for sums of them
+        off_by = 16 * 2.0**-11 * (got.double() * u).norm() + 1e-6 * want.abs()
+        assert (want - (got.double() * u).sum()).abs() <= off_by, which
+
+
+def test_expert_block_serves_as_the_paged_layer(D):
+    """The same weights in a paged layer: the same choice and weights, bit for
+    bit, and outputs that differ by their roundings alone."""
+    import numpy as np
+
+    from host_paged_expert_gb300 import _lib, synth
+
+    s = synth.TINY
+    H, E, I, k, T = s.hidden, s.num_experts, s.intermediate, s.top_k, 24
+    moe = _lib.PagedMoE(s, max_tokens=T)
+    w13, w2 = rand(E, 2 * I, H, seed=1, scale=H**-0.5), rand(E, H, I, seed=2, scale=I**-0.5)
+    bits = lambda t: t.view(torch.int16).cpu().numpy().view(np.uint16)  # noqa: E731
+    for e in range(E):
+        moe.load_expert(0, e, {"w13": bits(w13[e]), "w2": bits(w2[e])})
+    x, logits = rand(T, H, seed=3), rand(T, E, seed=4, dt=F32)
+    paged = moe.forward(0, x, logits)
+    torch.cuda.synchronize()
+    plan = moe.read_plan(0, T)
+    r = D.route(logits, k)
+    assert np.array_equal(plan["topk_id"].reshape(T, k), r.ids.cpu().numpy())
+    assert np.array_equal(plan["topk_w"].reshape(T, k).view(np.int32), r.weights.cpu().numpy().view(np.int32))
+    y = D.grouped_ffn(D.expand_rows(x, r.place), w13, w2, r.offsets)
+    out = D.combine_rows(y, r.place, r.weights)
+    # h in 16 bits or not, y in 16 bits or not, the result's rounding on both sides
+    a, p = out.double(), paged.double()
+    assert ((a - p).norm(dim=1) / p.norm(dim=1)).max() <= 4 * 2.0**-8
+    moe.close()
+
+
+def test_expert_block_captured(D):
+    b = _block()
+    x, dout = rand(64, 128, seed=9), rand(64, 128, seed=10)
+
+    def step():
+        out, saved = b.forward(x)
+        dx, g = b.backward(dout, saved)
+        return [out, dx, *g.values()]
+
+    ref = step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    x.copy_(rand(64, 128, seed=11))
+    g.replay()
+    torch.cuda.synchronize()
+    assert not same(got[0], ref[0])
+    assert all(same(p, q) for p, q in zip(got, step()))
