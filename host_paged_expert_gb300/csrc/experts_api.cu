@@ -19,7 +19,7 @@ bool entries_fit(int64_t tokens, int64_t k) { return tokens * k <= INT32_MAX; }
 // ---- route
 
 extern "C" size_t pe_route_workspace(int32_t tokens, int32_t experts) {
-    if (tokens <= 0 || experts <= 0) return 0;
+    if (tokens <= 0 || experts <= 0 || route_chunks(tokens) == 1) return 0;  // one block needs none
     return up256(sizeof(int32_t) * (size_t)route_chunks(tokens) * experts);
 }
 
@@ -35,7 +35,8 @@ extern "C" pe_status pe_route(const float* logits, int64_t logits_stride, int32_
         return bad("pe_route: pointers must be 4-byte aligned");
     if (tokens == 0) return done(cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (size_t)(experts + 1), stream_of(stream)));
     if (logits_stride < experts || logits_stride >= (int64_t(1) << 36)) return bad("pe_route: the logits' row pitch must be at least experts");
-    if (workspace_bytes < pe_route_workspace(tokens, experts) || !workspace) return bad("pe_route: workspace too small");
+    const size_t need = pe_route_workspace(tokens, experts);
+    if (workspace_bytes < need || (need && !workspace)) return bad("pe_route: workspace too small");
     if (!aligned(workspace)) return bad("pe_route: the workspace must be 16-byte aligned");
     RouteArgs a = {logits, logits_stride, ids, weights, offsets, place, static_cast<int32_t*>(workspace), tokens, experts, top_k};
     return done(launch_route_tokens(a, stream_of(stream)));

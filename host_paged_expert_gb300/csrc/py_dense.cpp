@@ -433,7 +433,9 @@ PyObject* route(PyObject* self, Args args, Py_ssize_t n) {
     if (away(args[2], x.dev)) return go_there(self, "route", x.dev, args, n);
     const size_t bytes = pe_route_workspace((int32_t)x.d0, (int32_t)x.d1);
     const at::Tensor ids = empty(x.dev, kI32, x.d0, k), w = empty(x.dev, kF32, x.d0, k), off = empty(x.dev, kI32, x.d1 + 1),
-                     place = empty(x.dev, kI32, x.d0, k), ws = empty(x.dev, kU8, (int64_t)bytes);
+                     place = empty(x.dev, kI32, x.d0, k);
+    at::Tensor ws;
+    if (bytes) ws = empty(x.dev, kU8, (int64_t)bytes);
     call([&] {
         return pe_route((const float*)x.p, x.s0, (int32_t*)ptr(ids), (float*)ptr(w), (int32_t*)ptr(off), (int32_t*)ptr(place), ptr(ws), bytes,
                         (int32_t)x.d0, (int32_t)k, (int32_t)x.d1, current(x.dev));

@@ -118,8 +118,8 @@ def test_gradients_are_not_dropped_without_a_word(call):
 
 A, N = 1 << 20, None
 MOST = (1 << 31) - (1 << 16)
-GOOD = {  # name: arguments at 4 tokens or rows
-    "pe_route": (A, 16, A, A, A, A, A, 1 << 40, 4, 2, 16, N),
+GOOD = {  # name: arguments at 4 tokens or rows (40 for pe_route, which then needs a workspace)
+    "pe_route": (A, 16, A, A, A, A, A, 1 << 40, 40, 2, 16, N),
     "pe_route_backward": (A, A, A, A, 4, 2, 16, N),
     "pe_expand_rows": (A, 64, A, A, 4, 2, 8, 64, 0, N),
     "pe_combine_rows": (A, 64, A, A, A, 64, A, 4, 2, 8, 64, 0, N),
@@ -181,6 +181,7 @@ def test_workspaces(L):
     assert L.pe_grouped_ffn_workspace(100, 40) == up(2 * 100 * 40)
     assert L.pe_grouped_ffn_backward_workspace(100, 40) == up(4 * 100 * 40) + up(2 * 100 * 40)
     # never more chunks of tokens than a launch has blocks for
-    for tokens in (1, 31, 32, 33, 5000, 1 << 20, 1 << 30):
+    assert L.pe_route_workspace(32, 128) == 0  # one block
+    for tokens in (33, 64, 5000, 1 << 20, 1 << 30):
         assert 0 < L.pe_route_workspace(tokens, 128) <= up(152 * 128 * 4)
     assert L.pe_route_workspace(0, 128) == L.pe_grouped_ffn_workspace(0, 8) == 0
