@@ -631,3 +631,54 @@ def test_expert_block_captured(D):
     torch.cuda.synchronize()
     assert not same(got[0], ref[0])
     assert all(same(p, q) for p, q in zip(got, step()))
+
+
+def test_two_host_threads(D):
+    """Calls from two threads on two streams: each its own results."""
+    import threading
+
+    run = _calls(D)
+    ref = run()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(10):
+                got = run()
+                st.synchronize()
+                if not all(same(a, b) for a, b in zip(ref, got)):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_products_behind_what_writes_their_arguments(D):
+    """A launch right before that makes the weights, the offsets or the rows: a
+    block that is there early reads none of them."""
+    sizes = [100, 0, 30, 70]
+    rows, k, n = 200, 256, 264
+    x, w, off = rand(rows, k), rand(4, n, k, seed=1, scale=0.1), offsets_of(sizes)
+    c, s, _ = weights("int4", n, k)
+    lg = rand(rows, 8, dt=F32)
+    ref = [D.grouped_linear(x, w, off), D.linear_w4(x[:5], c, s, "int4"), D.linear_w4(x[:40], c, s, "int4"), *D.route(lg, 2)]
+    x2, w2, off2, c2, lg2 = (torch.zeros_like(t) for t in (x, w, off, c, lg))
+    for _ in range(20):
+        for t in (x2, w2, off2, c2, lg2):
+            t.zero_()
+        x2.copy_(x), w2.copy_(w), off2.copy_(off)
+        got = [D.grouped_linear(x2, w2, off2)]
+        c2.copy_(c)
+        got.append(D.linear_w4(x2[:5], c2, s, "int4"))
+        c2.zero_()
+        c2.copy_(c)
+        got.append(D.linear_w4(x2[:40], c2, s, "int4"))
+        lg2.copy_(lg)
+        got += D.route(lg2, 2)
+        assert all(same(a, b) for a, b in zip(ref, got))
