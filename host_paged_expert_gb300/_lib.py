@@ -37,7 +37,7 @@ EXPORTS = [
     "pe_route", "pe_route_workspace", "pe_route_backward", "pe_expand_rows", "pe_combine_rows",
     "pe_combine_rows_backward", "pe_grouped_linear", "pe_grouped_linear_backward", "pe_grouped_ffn",
     "pe_grouped_ffn_workspace", "pe_grouped_ffn_backward", "pe_grouped_ffn_backward_workspace",
-    "pe_linear_four_bit", "pe_linear_four_bit_workspace",
+    "pe_linear_four_bit", "pe_linear_four_bit_workspace", "pe_selftest_experts_waits",
 ]
 
 
@@ -135,6 +135,7 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).restype = c_size_t
     L.pe_dense_error.argtypes = [POINTER(c_uint32)]
     L.pe_selftest_dense_waits.argtypes = [c_uint32, P, N, POINTER(c_uint32)]
+    L.pe_selftest_experts_waits.argtypes = [c_uint32, P, N, POINTER(c_uint32)]
     L.pe_last_error.argtypes = [c_void_p]
     L.pe_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:

@@ -73,7 +73,8 @@ struct Grouped {
     int depth;       // K (GROUP_WEIGHTS: N)
     Epi e;           // out, act, keep, gu, h; rows and columns are the kernel's
 };
-cudaError_t launch_grouped(const Grouped& p, GroupKind kind, int elem, uint32_t* err, cudaStream_t st);
+cudaError_t launch_grouped(const Grouped& p, GroupKind kind, int elem, uint32_t* err, cudaStream_t st,
+                           const WaitLimits* limits = nullptr);
 
 // ---- 4-bit weights
 
@@ -92,7 +93,7 @@ struct W4Args {
 // into shared memory; above, the weights are unpacked first.
 constexpr int kW4Stream = 16, kW4Rows = 128;
 cudaError_t launch_w4(const W4Args& a, int elem, cudaStream_t st);
-cudaError_t launch_w4_tc(const W4Args& a, int elem, uint32_t* err, cudaStream_t st);
+cudaError_t launch_w4_tc(const W4Args& a, int elem, uint32_t* err, cudaStream_t st, const WaitLimits* limits = nullptr);
 // w [N, K] of the element type = codes times scales
 cudaError_t launch_w4_unpack(const W4Args& a, void* w, int elem, cudaStream_t st);
 

@@ -404,3 +404,55 @@ extern "C" pe_status pe_linear_four_bit(const void* x, int64_t x_stride, const v
     }
     return done(e);
 }
+
+// ---- self-test
+
+extern "C" pe_status pe_selftest_experts_waits(uint32_t poll_limit, void* scratch, size_t scratch_bytes, uint32_t* out_words) {
+    if (!out_words || !scratch || poll_limit == 0) return bad("pe_selftest_experts_waits: NULL pointer or no polls");
+    if (scratch_bytes < PE_SELFTEST_EXPERTS_BYTES || !aligned(scratch, 256))
+        return bad("pe_selftest_experts_waits: scratch too small or not 256-byte aligned");
+    // operands and scales are zeros; one group; a word of its own for each run
+    constexpr int R = 1000, N = 256, K = 1024, T = 32, K4 = 4096;  // a tail of rows, more blocks than stages
+    constexpr int kTileRows = 128;
+    constexpr size_t kOperand = 2 * (size_t)K * K, kRuns = 12;
+    static_assert(2 * R * N <= (int)kOperand && T * K4 * 2 <= (int)kOperand && 512 + kOperand + 4 * N * K <= PE_SELFTEST_EXPERTS_BYTES, "the scratch holds them");
+    uint8_t* base = static_cast<uint8_t*>(scratch);
+    uint32_t* words = reinterpret_cast<uint32_t*>(base);
+    int32_t* offsets = reinterpret_cast<int32_t*>(base + 256);
+    uint8_t *ops = base + 512, *out = ops + kOperand;
+    const int32_t ends[2] = {0, R};
+    cudaError_t e = cudaMemset(scratch, 0, PE_SELFTEST_EXPERTS_BYTES);
+    if (!e) e = cudaMemcpy(offsets, ends, sizeof ends, cudaMemcpyHostToDevice);
+    // one role gives up at once, the others after poll_limit polls
+    const WaitLimits gives_up[3] = {{poll_limit, 0, poll_limit}, {poll_limit, poll_limit, 0}, {0, poll_limit, poll_limit}};
+    for (size_t i = 0; !e && i < kRuns; ++i) {
+        const WaitLimits* limits = &gives_up[i % 3];
+        if (i < 9) {
+            const GroupKind kind = i < 3 ? GROUP_ROWS : i < 6 ? GROUP_GATED : GROUP_WEIGHTS;
+            // rows in no group past K, the operands' ends
+            Grouped p = kind == GROUP_WEIGHTS ? gradient(ops, N, ops, N, offsets, R, 1, N, N, out)
+                                              : product(ops, 0, ops, K, offsets, N, 1, kind == GROUP_GATED ? N / 2 : N, K);
+            p.e.out = out;
+            p.e.ld_out = N;
+            e = launch_grouped(p, kind, PE_ELEM_BF16, words + i, 0, limits);
+        } else {
+            W4Args a = {};
+            a.x = ops;
+            a.ld_x = K4;
+            a.codes = ops;
+            a.scales = ops;
+            a.M = T;
+            a.N = kTileRows;
+            a.K = K4;
+            a.e.rows = T;
+            a.e.cols = kTileRows;
+            a.e.vec = 1;
+            a.e.out = out;
+            a.e.ld_out = kTileRows;
+            e = launch_w4_tc(a, PE_ELEM_BF16, words + i, 0, limits);
+        }
+    }
+    if (!e) e = cudaDeviceSynchronize();
+    if (!e) e = cudaMemcpy(out_words, words, kRuns * sizeof(uint32_t), cudaMemcpyDeviceToHost);
+    return done(e);
+}

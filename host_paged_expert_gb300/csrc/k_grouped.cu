@@ -54,6 +54,7 @@ struct Work {
     Divide across;     // by ftiles (GROUP_WEIGHTS: by a group's tiles)
     Divide down;       // GROUP_WEIGHTS: by ftiles
     int stages;
+    WaitLimits limit;
     Epi e;
 };
 
@@ -244,10 +245,12 @@ struct Before<E, GROUP_GATED_BWD> {
     }
 };
 
-template <typename E, int KIND>
+// LIMITED: the waits' limits are the launch's.
+template <typename E, int KIND, bool LIMITED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ Work w, uint32_t* err) {
     constexpr bool WEIGHTS = KIND == GROUP_WEIGHTS, GATED = KIND == GROUP_GATED;
     constexpr int BK = 64;
+    auto polls = [](uint32_t limit) { return LIMITED ? limit : kPolls; };
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -300,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             const int blocks = (tl.kn + BK - 1) / BK, early = early_at<WEIGHTS>(tl.kn);
             for (int j = 0; j < blocks; ++j) {
                 const int k = (!WEIGHTS || j < early ? j : j == early ? blocks - 1 : j - 1) * BK;
-                if (!(ok = tc::mbar_spin(&S.empty[s], phase, err, kPolls))) break;
+                if (!(ok = tc::mbar_spin(&S.empty[s], phase, err, polls(w.limit.copies)))) break;
                 if (lead) {
                     uint8_t* a = ring + s * kStage;
                     uint8_t* b = a + kOperand;
@@ -343,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         // The leader's MMAs arrive on this CTA's barriers: stay until the last of
         // them have (a stage never used passes at once).
         for (int i = 0; ok && i < w.stages; ++i) {
-            ok = tc::mbar_spin(&S.empty[s], phase, err, kPolls);
+            ok = tc::mbar_spin(&S.empty[s], phase, err, polls(w.limit.copies));
             if (++s == (uint32_t)w.stages) s = 0, phase ^= 1;
         }
         if (!ok) tc::settle();  // copies may be on their way
@@ -360,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             const Tile tl = walk.at(w);
             if (tl.kn <= 0) continue;  // zeros
             const uint32_t id = tc::idesc(FMT, a_mn, b_mn, kTile, tl.nt);
-            if (!(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, kPolls))) break;
+            if (!(ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, polls(w.limit.mma)))) break;
             const int blocks = (tl.kn + BK - 1) / BK, early = early_at<WEIGHTS>(tl.kn);
             uint32_t s_tail = 0, phase_tail = 0;
             for (int j = 0; j < blocks; ++j) {
@@ -370,7 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 }
                 const bool last = j == blocks - 1, late = WEIGHTS && last && early < blocks - 1;
                 const uint32_t at = late ? s_tail : s, ph = late ? phase_tail : phase;
-                if (!(ok = WEIGHTS ? tc::mbar_spin_cluster(&S.full[at], ph, err, kPolls) : tc::mbar_spin(&S.full[at], ph, err, kPolls))) break;
+                const uint32_t limit = polls(w.limit.mma);
+                if (!(ok = WEIGHTS ? tc::mbar_spin_cluster(&S.full[at], ph, err, limit) : tc::mbar_spin(&S.full[at], ph, err, limit))) break;
                 tc::fence_after_sync();
                 if (lead) {
                     const uint64_t a = a0 + at * (kStage >> 4), b = b0 + at * (kStage >> 4);
@@ -389,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
         }
         // the other CTA's epilogue warps arrive here too: stay until the last of them have
         for (int i = 0; ok && i < 2; ++i) {
-            ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, kPolls);
+            ok = tc::mbar_spin(&S.acc_empty[buf], buf_phase, err, polls(w.limit.mma));
             buf ^= 1;
             if (buf == 0) buf_phase ^= 1;
         }
@@ -407,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
             const int blocks = (tl.kn + BK - 1) / BK, rem = tl.kn % BK;
             if (rem) {
                 const uint32_t at = (s + early_at<true>(tl.kn)) % w.stages;
-                if (!(ok = tc::mbar_spin(&S.raw[at], phases >> at & 1, err, kPolls))) break;
+                if (!(ok = tc::mbar_spin(&S.raw[at], phases >> at & 1, err, polls(w.limit.copies)))) break;
                 phases ^= 1u << at;
                 // a row along K is 128 bytes of each of four boxes
                 uint8_t* to = ring + at * kStage + (lane >> 3) * 8192 + (lane & 7) * 16;
@@ -437,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 // it, stored by TMA, which leaves out what is past the result
                 const int m = tl.f * kTile + (int)rank * kHalf + quarter * 32;
                 if (tl.kn > 0) {
-                    if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, kPolls))) break;
+                    if (!(ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, polls(w.limit.sums)))) break;
                     ++use_acc;
                     tc::fence_after_sync();
                 }
@@ -478,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) grouped
                 Epi e = w.e;
                 e.rows = tl.end;
                 const int live = min(tl.nt, tl.end - tl.n0);  // rows of this tile
-                ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, kPolls);
+                ok = tc::mbar_spin(&S.acc_full[buf], (use_acc >> 1) & 1, err, polls(w.limit.sums));
                 const int couple = 1 + half * 2 + (quarter & 1);
                 if (GATED) ok = couple_and(couple, ok);
                 if (!ok) break;
@@ -558,14 +562,14 @@ int stages_of(GroupKind kind, int groups) {
 }
 
 // Pairs that the device holds at once, looked up once per kernel.
-template <typename E, int KIND>
+template <typename E, int KIND, bool LIMITED>
 cudaError_t resident_pairs(int* out) {
     static std::atomic<int> known[64];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     int n = dev < 64 ? known[dev].load() : 0;
     if (!n) {
-        auto k = grouped_kernel<E, KIND>;
+        auto k = grouped_kernel<E, KIND, LIMITED>;
         const int bytes = kSmem - (int)sizeof(Shared);
         if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
         cudaLaunchConfig_t cfg = {};
@@ -580,8 +584,8 @@ cudaError_t resident_pairs(int* out) {
     return cudaSuccess;
 }
 
-template <typename E, int KIND>
-cudaError_t launch(const Grouped& p, uint32_t* err, cudaStream_t st) {
+template <typename E, int KIND, bool LIMITED = false>
+cudaError_t launch(const Grouped& p, uint32_t* err, cudaStream_t st, const WaitLimits& limits = {}) {
     constexpr bool WEIGHTS = KIND == GROUP_WEIGHTS;
     constexpr int NF = KIND == GROUP_GATED ? kHalf : kTile;
     Work w = {};
@@ -614,6 +618,7 @@ cudaError_t launch(const Grouped& p, uint32_t* err, cudaStream_t st) {
     w.across = Divide::by(WEIGHTS ? w.ftiles * w.ntiles : w.ftiles);
     w.down = Divide::by(w.ftiles);
     w.stages = stages_of((GroupKind)KIND, p.groups);
+    w.limit = limits;
     w.e = p.e;
     w.e.cols = p.features;
     w.e.vec = 1;
@@ -622,10 +627,10 @@ cudaError_t launch(const Grouped& p, uint32_t* err, cudaStream_t st) {
                                    : ((long long)p.rows / kTile + (p.groups < p.rows ? p.groups : p.rows)) * w.ftiles;
     if (most > INT_MAX / 2 || w.stages < 2) return cudaErrorInvalidValue;
     int pairs = 0;
-    if (cudaError_t e = resident_pairs<E, KIND>(&pairs)) return e;
+    if (cudaError_t e = resident_pairs<E, KIND, LIMITED>(&pairs)) return e;
     if (most < pairs) pairs = (int)most;
     const int bytes = 1024 + w.stages * kStage + kEpiWarps * patch_bytes(KIND) + table_bytes(p.groups);
-    return launch_pdl(grouped_kernel<E, KIND>, dim3(2 * pairs), dim3(kThreads), bytes, st, w, err);
+    return launch_pdl(grouped_kernel<E, KIND, LIMITED>, dim3(2 * pairs), dim3(kThreads), bytes, st, w, err);
 }
 
 template <typename E>
@@ -640,7 +645,11 @@ cudaError_t launch_kind(const Grouped& p, GroupKind kind, uint32_t* err, cudaStr
 
 }  // namespace
 
-cudaError_t launch_grouped(const Grouped& p, GroupKind kind, int elem, uint32_t* err, cudaStream_t st) {
+cudaError_t launch_grouped(const Grouped& p, GroupKind kind, int elem, uint32_t* err, cudaStream_t st, const WaitLimits* limits) {
+    if (limits)
+        return kind == GROUP_WEIGHTS ? launch<__nv_bfloat16, GROUP_WEIGHTS, true>(p, err, st, *limits)
+               : kind == GROUP_GATED ? launch<__nv_bfloat16, GROUP_GATED, true>(p, err, st, *limits)
+                                     : launch<__nv_bfloat16, GROUP_ROWS, true>(p, err, st, *limits);
     return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, err, st) : launch_kind<__half>(p, kind, err, st);
 }
 

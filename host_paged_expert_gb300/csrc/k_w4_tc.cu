@@ -41,6 +41,7 @@ constexpr int kMostTokens = 64;
 struct Plan {
     int nt, q_bytes;  // tokens of a tile, a multiple of 16; bytes of their block
     int split, ftiles;
+    WaitLimits limit;
 };
 struct Shared {
     uint64_t full[kStages], done[kStages], acc_empty[kStages], drain;
@@ -55,9 +56,11 @@ struct Codes {
     uint32_t s[2];
 };
 
-template <typename E, int FMT>
+// LIMITED: the waits' limits are the launch's.
+template <typename E, int FMT, bool LIMITED>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ W4Args a, const __grid_constant__ Plan q, uint32_t* err) {
+    auto polls = [](uint32_t limit) { return LIMITED ? limit : kPolls; };
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int p = 0;
         for (; p < np; ++p) {
             const int s = p % kStages;
-            if (!(ok = tc::mbar_spin(&S.done[s], (p / kStages & 1) ^ 1, err, kPolls))) break;
+            if (!(ok = tc::mbar_spin(&S.done[s], (p / kStages & 1) ^ 1, err, polls(q.limit.copies)))) break;
             if (lead) {
                 uint8_t* to = ring + s * stage + 2 * kP;
                 tc::mbar_arrive_expect_tx(&S.full[s], 2 * q.q_bytes);
@@ -115,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), false), b0 = tc::operand_desc(tc::smem_u32(ring) + 2 * kP, false);
         for (int p = 0; p < np; ++p) {
             const int s = p % kStages;
-            if (!tc::mbar_spin(&S.acc_empty[s], (p / kStages & 1) ^ 1, err, kPolls)) break;
-            if (!tc::mbar_spin(&S.full[s], p / kStages & 1, err, kPolls)) break;
+            if (!tc::mbar_spin(&S.acc_empty[s], (p / kStages & 1) ^ 1, err, polls(q.limit.mma))) break;
+            if (!tc::mbar_spin(&S.full[s], p / kStages & 1, err, polls(q.limit.mma))) break;
             tc::fence_after_sync();
             if (lead) {
                 const uint64_t da = a0 + (uint32_t)(s * stage >> 4), db = b0 + (uint32_t)(s * stage >> 4);
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float s = FMT == W4_INT4 ? __half2float(__ushort_as_half(next)) : 1.f;
             if (FMT == W4_INT4 && p + 1 < np) next = scales[p + 1];
             const int buf = p % kStages;
-            if (!(ok = tc::mbar_spin(&S.done[buf], p / kStages & 1, err, kPolls))) break;
+            if (!(ok = tc::mbar_spin(&S.done[buf], p / kStages & 1, err, polls(q.limit.sums)))) break;
             tc::fence_after_sync();
             if (c0 < q.nt) {
 #pragma unroll
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < kAhead; ++h) {
                 const int p = pb + 2 * h;
                 if (!ok || p >= np) continue;
-                ok = tc::mbar_spin(&S.done[s], phase, err, kPolls);
+                ok = tc::mbar_spin(&S.done[s], phase, err, polls(q.limit.copies));
                 if (!ok) continue;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -261,18 +264,19 @@ int split_of(int tiles, int pairs) {
     return n;
 }
 
-template <typename E, int FMT>
-cudaError_t launch(const W4Args& a, uint32_t* err, cudaStream_t st) {
+template <typename E, int FMT, bool LIMITED = false>
+cudaError_t launch(const W4Args& a, uint32_t* err, cudaStream_t st, const WaitLimits& limits = {}) {
     static std::atomic<uint64_t> ready;  // devices whose attribute is set
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    auto kernel = w4_tc_kernel<E, FMT>;
+    auto kernel = w4_tc_kernel<E, FMT, LIMITED>;
     constexpr int most = 1024 + kStages * 2 * (kP + kMostTokens * 128);
     if (dev >= 64 || !(ready.load() >> dev & 1)) {
         if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) return e;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
     }
     Plan q = {};
+    q.limit = limits;
     const int ttiles = (a.M + kMostTokens - 1) / kMostTokens;
     if ((long long)((a.N + kRows - 1) / kRows) * ttiles > INT_MAX / 4) return cudaErrorInvalidValue;
     q.nt = ((a.M + ttiles - 1) / ttiles + 15) / 16 * 16;
@@ -304,7 +308,8 @@ cudaError_t by_format(const W4Args& a, uint32_t* err, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_w4_tc(const W4Args& a, int elem, uint32_t* err, cudaStream_t st) {
+cudaError_t launch_w4_tc(const W4Args& a, int elem, uint32_t* err, cudaStream_t st, const WaitLimits* limits) {
+    if (limits) return launch<__nv_bfloat16, W4_INT4, true>(a, err, st, *limits);
     return elem == PE_ELEM_BF16 ? by_format<__nv_bfloat16>(a, err, st) : by_format<__half>(a, err, st);
 }
 

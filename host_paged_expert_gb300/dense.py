@@ -100,16 +100,25 @@ def error_word() -> int:
     return int(w.value)
 
 
-def selftest_waits(poll_limit: int = 1 << 12) -> list[int]:
-    """Error words of the twelve runs of pe_selftest_dense_waits (each must
-    read PE_DEVERR_TIMEOUT).  Synchronises the device."""
-    scratch = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+def _selftest(call, poll_limit: int, scratch_bytes: int) -> list[int]:
+    scratch = torch.empty(scratch_bytes, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     out = (ctypes.c_uint32 * 12)()
-    st = lib().pe_selftest_dense_waits(poll_limit, scratch.data_ptr(), scratch.numel(), out)
+    st = call(poll_limit, scratch.data_ptr(), scratch.numel(), out)
     if st:
         _raise(st, lib().pe_last_error(None).decode())
     return list(out)
+
+
+def selftest_waits(poll_limit: int = 1 << 12) -> list[int]:
+    """Error words of the twelve runs of pe_selftest_dense_waits (each must
+    read PE_DEVERR_TIMEOUT).  Synchronises the device."""
+    return _selftest(lib().pe_selftest_dense_waits, poll_limit, 1 << 20)
+
+
+def selftest_expert_waits(poll_limit: int = 1 << 12) -> list[int]:
+    """The same of pe_selftest_experts_waits."""
+    return _selftest(lib().pe_selftest_experts_waits, poll_limit, 4 << 20)
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, *, y: bool = True, quant: bool = False, save: bool = False,

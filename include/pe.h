@@ -597,6 +597,14 @@ pe_status pe_dense_error(uint32_t* word);
 #define PE_SELFTEST_DENSE_BYTES (1u << 20)
 pe_status pe_selftest_dense_waits(uint32_t poll_limit, void* scratch, size_t scratch_bytes, uint32_t* out12);
 
+/* The same for the kernels of grouped products and of 4-bit weights: products of
+ * one group (out_words[0..2]), with gate and up (3..5), weight gradients (6..8) and
+ * 32 rows of 4-bit weights (9..11), the role that gives up as above.
+ * scratch: PE_SELFTEST_EXPERTS_BYTES of device memory, 256-byte aligned;
+ * out_words: 12 words on the host. */
+#define PE_SELFTEST_EXPERTS_BYTES (4u << 20)
+pe_status pe_selftest_experts_waits(uint32_t poll_limit, void* scratch, size_t scratch_bytes, uint32_t* out_words);
+
 /* Frees the host store (if owned) and the handle; never the arena. */
 void pe_destroy(pe_handle* h);
 

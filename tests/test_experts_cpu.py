@@ -185,3 +185,12 @@ def test_workspaces(L):
     for tokens in (33, 64, 5000, 1 << 20, 1 << 30):
         assert 0 < L.pe_route_workspace(tokens, 128) <= up(152 * 128 * 4)
     assert L.pe_route_workspace(0, 128) == L.pe_grouped_ffn_workspace(0, 8) == 0
+
+
+def test_selftest_of_the_waits_refuses(L):
+    import ctypes
+
+    out = (ctypes.c_uint32 * 12)()
+    call = L.pe_selftest_experts_waits
+    assert [call(0, A, 4 << 20, out), call(9, None, 4 << 20, out), call(9, A, (4 << 20) - 1, out), call(9, A + 16, 4 << 20, out),
+            call(9, A, 4 << 20, None)] == [INVALID] * 5

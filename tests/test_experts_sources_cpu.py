@@ -45,6 +45,14 @@ def test_cleared_tails_are_handed_over():
     assert "WEIGHTS ? tc::mbar_spin_cluster(&S.full[at]" in text
 
 
+@pytest.mark.parametrize("name", ["k_grouped.cu", "k_w4_tc.cu"])
+def test_every_wait_of_a_role_has_the_launchs_limit(name):
+    """So that the self-test can make each of them run out."""
+    text = code(name)
+    assert text.count("mbar_spin") >= 5 and text.count("polls(") >= 5
+    assert not re.findall(r"err,\s*kPolls", text)
+
+
 def test_split_weights_wait_for_the_launch_before():
     """The kernel of 17 to 128 rows counts its polls once the launch before is done."""
     text = code("k_w4_tc.cu")

@@ -682,3 +682,15 @@ def test_products_behind_what_writes_their_arguments(D):
         lg2.copy_(lg)
         got += D.route(lg2, 2)
         assert all(same(a, b) for a, b in zip(ref, got))
+
+
+def test_waits_that_run_out(D):
+    """Each role of each kernel in turn gives up: the others follow, nothing
+    hangs, and the calls after it are right."""
+    for polls in (1, 1 << 12):
+        assert D.selftest_expert_waits(polls) == [0x8] * 12  # PE_DEVERR_TIMEOUT
+    assert D.error_word() == 0
+    x, off, w = rand(60, 128), offsets_of([10, 0, 50]), rand(3, 72, 128, seed=1)
+    R.check(D.grouped_linear(x, w, off), X.grouped_linear(x, w, off, BF), "y")
+    c, s, _ = weights("int4", 72, 128)
+    R.check(D.linear_w4(x, c, s, "int4"), X.linear_w4(x, X.values(c, s, "int4"), None, "none", None, BF, BF, False), "w4")
