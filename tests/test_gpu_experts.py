@@ -694,3 +694,56 @@ def test_waits_that_run_out(D):
     R.check(D.grouped_linear(x, w, off), X.grouped_linear(x, w, off, BF), "y")
     c, s, _ = weights("int4", 72, 128)
     R.check(D.linear_w4(x, c, s, "int4"), X.linear_w4(x, X.values(c, s, "int4"), None, "none", None, BF, BF, False), "w4")
+
+
+def test_each_gradient_alone(D):
+    """What the C calls leave out on request changes nothing of the rest."""
+    from host_paged_expert_gb300._lib import lib
+
+    L, st = lib(), torch.cuda.current_stream().cuda_stream
+    sizes, h, i = [5, 0, 70, 33], 136, 72
+    rows, g, off = sum(sizes), len(sizes), offsets_of(sizes)
+    x, w13, w2, dy = rand(rows, h), rand(g, 2 * i, h, seed=1, scale=0.1), rand(g, h, i, seed=2, scale=0.1), rand(rows, h, seed=3)
+    _, gu = D.grouped_ffn(x, w13, w2, off, save=True)
+    want = D.grouped_ffn_backward(dy, x, w13, w2, gu, off)
+    ws = torch.empty(L.pe_grouped_ffn_backward_workspace(rows, i), dtype=torch.uint8, device="cuda")
+    for which in range(3):
+        out = torch.full_like(want[which], 7.0)
+        at = [out.data_ptr() if j == which else None for j in range(3)]
+        assert L.pe_grouped_ffn_backward(dy.data_ptr(), h, x.data_ptr(), h, w13.data_ptr(), w2.data_ptr(), gu.data_ptr(), off.data_ptr(), 1, *at, ws.data_ptr(),
+                                         ws.numel(), rows, g, h, i, 0, st) == 0
+        assert same(out, want[which])
+    w, dz = rand(g, 72, h, seed=4), rand(rows, 72, seed=5)
+    want = D.grouped_linear_backward(dz, x, w, off)
+    for which in range(2):
+        out = torch.full_like(want[which], 7.0)
+        at = [out.data_ptr() if j == which else None for j in range(2)]
+        assert L.pe_grouped_linear_backward(dz.data_ptr(), 72, x.data_ptr(), h, w.data_ptr(), off.data_ptr(), *at, rows, g, h, 72, 0, st) == 0
+        assert same(out, want[which])
+    # the weighted sum's: without dweights, and then without y
+    place, wt = places(9, 3), rand(9, 3, dt=F32)
+    y, d = rand(27, h, seed=6), rand(9, h, seed=7)
+    want = D.combine_rows_backward(d, y, place, wt)[0]
+    out = torch.full_like(want, 7.0)
+    assert L.pe_combine_rows_backward(d.data_ptr(), h, None, 0, place.data_ptr(), wt.data_ptr(), out.data_ptr(), None, 9, 3, 27, h, 0, st) == 0
+    assert same(out, want)
+
+
+def test_many_groups_and_wide_features(D):
+    """The most groups that a call takes, and a table that leaves the ring a
+    stage less, in each kind of product."""
+    g, h, i = 1024, 72, 40
+    sizes = [(7 * j) % 5 for j in range(g)]
+    rows, off = sum(sizes), offsets_of(sizes)
+    x, w13, w2, dy = rand(rows, h), rand(g, 2 * i, h, seed=1, scale=0.1), rand(g, h, i, seed=2, scale=0.1), rand(rows, h, seed=3)
+    y, gu = D.grouped_ffn(x, w13, w2, off, save=True)
+    want = X.grouped_ffn(x, w13, w2, off, "silu", BF)
+    R.check(y, want["y"], "y")
+    R.check(gu, want["gu"], "gu")
+    want = X.grouped_ffn_backward(dy, x, w13, w2, gu, off, "silu", BF)
+    for v, name in zip(D.grouped_ffn_backward(dy, x, w13, w2, gu, off), ("dx", "dw13", "dw2")):
+        R.check(v, want[name], name)
+    # many feature tiles against one row
+    w = rand(2, 20000, 64, seed=4, scale=0.1)
+    off = offsets_of([1, 2])
+    R.check(D.grouped_linear(x[:3, :64], w, off), X.grouped_linear(x[:3, :64], w, off, BF), "wide")
