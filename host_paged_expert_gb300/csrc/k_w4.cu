@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const __grid_constant__ 
         const size_t at = (size_t)n * groups + k / w4_group(FMT);
         float s;
         if (FMT == W4_INT4) s = __half2float(static_cast<const __half*>(a.scales)[at]);
-        else if (FMT == W4_MXFP4) s = 0.5f * in_range<E>(e8m0(static_cast<const uint8_t*>(a.scales)[at]));
+        else if (FMT == W4_MXFP4) s = 0.5f * e8m0(static_cast<const uint8_t*>(a.scales)[at]);
         else s = 0.5f * ts * e4m3x2(static_cast<const uint8_t*>(a.scales)[at]).x;
         float v[8];
         if (FMT == W4_INT4) {

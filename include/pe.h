@@ -567,7 +567,8 @@ pe_status pe_grouped_ffn_backward(const void* dy, int64_t dy_stride, const void*
  * Up to 128 rows the weights are used unrounded (with fp16, MXFP4 scales above
  * 2^15 count as 2^15 and are lost below 2^-24); above, they are unpacked to elem
  * in the workspace first: int4's and NVFP4's products with their scales are
- * rounded there, and a weight beyond fp16's range is infinite.
+ * rounded there.  With fp16 a weight is then what fp16 holds of it: infinite
+ * from 65520 on, without its last bits below 2^-14, zero up to 2^-25.
  * in: a multiple of 32.
  * workspace: pe_linear_four_bit_workspace(rows, in, out) bytes. */
 size_t pe_linear_four_bit_workspace(int32_t rows, int32_t in_features, int32_t out_features);
