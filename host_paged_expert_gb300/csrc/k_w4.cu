@@ -23,8 +23,10 @@
 // Rounding: int4's q - 8 and E2M1 times its block scale are exact in 16 bits
 // (a 2-bit times a 4-bit significand, or a power of two), int4's scales
 // multiply fp32 sums of 128 inputs, and so does NVFP4's tensor scale in the
-// end: weights are not rounded at all.  Above kW4Rows the weights are unpacked to
-// 16 bits for the dense products' kernels, which rounds int4's and NVFP4's once.
+// end.  MXFP4's scales reach past fp16 at both ends: with it they multiply sums
+// of their 32 inputs, and a lane takes eight codes of each group instead of a
+// group's 32.  So weights are not rounded at all.  Above kW4Rows they are unpacked
+// to 16 bits for the dense products' kernels, which rounds int4's and NVFP4's once.
 #include "experts.cuh"
 #include "fp8_device.cuh"
 #include "pe_device.cuh"
@@ -50,19 +52,43 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // A warp's share of a 128-input chunk on its way: codes and raw scales of its
-// rows g and g + 8 of RT tiles, and the tokens' inputs.
+// rows g and g + 8 of RT tiles, and the tokens' inputs.  Where scales multiply
+// sums of 32 inputs (kScaleSums) word i of a lane's codes, and its inputs i, are of
+// group i: codes 32 i + 8 t .. 32 i + 8 t + 7 of the chunk.
 template <int RT, int NT>
 struct Chunk {
     int4 w[RT][2], x[4][NT];
     uint32_t s[RT][2];
 };
 
-// Asks for chunk c.  k: the first input of this lane's 32.
+__device__ __forceinline__ int& word_of(int4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Asks for chunk c.  k: the first input of this lane's 32.  K is a multiple of 32.
 template <typename E, int FMT, int RT, int NT>
 __device__ __forceinline__ void fetch(Chunk<RT, NT>& q, const uint8_t* const (&codes)[RT][2], const uint8_t* const (&scales)[RT][2],
                                       const E* const (&x)[NT], int K, int c, int k) {
-    const bool whole = (c + 1) * kChunk <= K;  // K is a multiple of 32: else some lanes have no inputs
-    if (whole || k < K) {
+    const bool whole = (c + 1) * kChunk <= K;
+    if constexpr (kScaleSums<E, FMT>) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool there = whole || c * kChunk + 32 * i < K;
+#pragma unroll
+            for (int m = 0; m < RT; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    word_of(q.w[m][r], i) = there ? *reinterpret_cast<const uint32_t*>(codes[m][r] + c * (kChunk / 2) + 16 * i) : 0;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                q.x[i][j] = there ? *reinterpret_cast<const int4*>(x[j] + c * kChunk + 32 * i) : make_int4(0, 0, 0, 0);
+        }
+        // a lane has one group's scale
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) q.s[m][r] = whole || k < K ? scales[m][r][c * (kChunk / 32)] : 0;
+        return;
+    }
+    if (whole || k < K) {  // else the lane has no inputs
 #pragma unroll
         for (int m = 0; m < RT; ++m)
 #pragma unroll
@@ -99,7 +125,7 @@ __device__ __forceinline__ void multiply(const Chunk<RT, NT>& q, float (&acc)[RT
             if (FMT == W4_INT4) {
                 s[m][r][0] = __half2float(__ushort_as_half((unsigned short)q.s[m][r]));
             } else if (FMT == W4_MXFP4) {
-                s[m][r][0] = s[m][r][1] = in_range<E>(e8m0(q.s[m][r]));
+                s[m][r][0] = s[m][r][1] = e8m0(q.s[m][r]);
             } else {
                 const float2 f = e4m3x2(q.s[m][r]);
                 s[m][r][0] = f.x, s[m][r][1] = f.y;
@@ -127,17 +153,27 @@ __device__ __forceinline__ void multiply(const Chunk<RT, NT>& q, float (&acc)[RT
             uint32_t p[2][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int4 w = q.w[m][r];
-                const uint32_t word = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+                int4 w = q.w[m][r];
+                const uint32_t word = word_of(w, i);
                 if (FMT == W4_INT4) int4x8<E>(word, p[r]);
+                else if (kScaleSums<E, FMT>) e2m1x8<E>(word, p[r]);
                 else e2m1x8<E>(word, Pair<E>::both(s[m][r][i / 2]), p[r]);
             }
             const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]}, a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                float(&d)[4] = FMT == W4_INT4 ? sum[m][j] : acc[m][j];
+                float(&d)[4] = FMT == W4_INT4 || kScaleSums<E, FMT> ? sum[m][j] : acc[m][j];
                 mma16816<E>(d, a0, b[j][0], b[j][1]);
                 mma16816<E>(d, a1, b[j][2], b[j][3]);
+            }
+            if constexpr (kScaleSums<E, FMT>) {  // the group's scale comes from the lane that has it
+                float f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) f[r] = __shfl_sync(0xffffffffu, s[m][r][0], i, 4);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) acc[m][j][h] = fmaf(f[h / 2], sum[m][j][h], acc[m][j][h]), sum[m][j][h] = 0.f;
             }
         }
     }
@@ -165,13 +201,13 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const __grid_constant__ W4Ar
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const size_t row = min(n0 + 16 * m + 8 * r + g, a.N - 1);
-            codes[m][r] = static_cast<const uint8_t*>(a.codes) + row * (a.K / 2) + 16 * t4;
+            codes[m][r] = static_cast<const uint8_t*>(a.codes) + row * (a.K / 2) + (kScaleSums<E, FMT> ? 4 : 16) * t4;
             scales[m][r] = static_cast<const uint8_t*>(a.scales) +
                            (FMT == W4_INT4 ? 2 * row * groups : row * groups + t4 * (FMT == W4_MXFP4 ? 1 : 2));
         }
     // columns of B without a token take another token's, and nobody takes their sums
 #pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] = static_cast<const E*>(a.x) + min(8 * j + g, a.M - 1) * a.ld_x + 32 * t4;
+    for (int j = 0; j < NT; ++j) x[j] = static_cast<const E*>(a.x) + min(8 * j + g, a.M - 1) * a.ld_x + (kScaleSums<E, FMT> ? 8 : 32) * t4;
     float acc[RT][NT][4] = {};
     pdl_wait();
     pdl_trigger();

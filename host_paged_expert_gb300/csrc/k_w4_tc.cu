@@ -12,7 +12,8 @@
 // Each pair, 128 inputs, has a TMEM buffer of its own.  Eight more warps add it
 // to fp32 registers, where a lane has a weight row: int4's group scale multiplies
 // it there, so int4's weights are not rounded, and E2M1 times its block scale is
-// exact in 16 bits.
+// exact in 16 bits.  But MXFP4's scales reach past fp16: with it a pair has four
+// buffers, one for each 32 inputs, and their scales multiply them too.
 //
 // Bound by the MMAs, which take about 110 cycles for 128 rows and 16 inputs
 // whatever the tokens, 0.48 of a pair's 0.53 us (without decoding anything it
@@ -34,9 +35,15 @@ namespace {
 constexpr int kDecoders = 8;  // warps that decode a pair of blocks, of which two sets take every other one
 constexpr int kThreads = 384 + 64 * kDecoders;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..11 sums, 12..27 decoding; all of them add up
 constexpr int kP = kRows * 128;  // bytes of a block of weights: 128 rows of 64 inputs
-constexpr int kStages = 4;       // of a pair of blocks each, and buffers of their sums in TMEM
+constexpr int kStages = 4;       // of a pair of blocks each
 constexpr int kAhead = 2;        // pairs of blocks whose codes are on their way to a thread
 constexpr int kMostTokens = 64;
+// Sums of a pair of blocks that have scales of their own (kScaleSums: of each 32
+// inputs), and places for such sums in TMEM.
+template <typename E, int FMT>
+constexpr int kSums = kScaleSums<E, FMT> ? 4 : 1;
+template <typename E, int FMT>
+constexpr int kPlaces = kScaleSums<E, FMT> ? 2 : kStages;
 
 struct Plan {
     int nt, q_bytes;  // tokens of a tile, a multiple of 16; bytes of their block
@@ -61,6 +68,7 @@ template <typename E, int FMT, bool LIMITED>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ W4Args a, const __grid_constant__ Plan q, uint32_t* err) {
     auto polls = [](uint32_t limit) { return LIMITED ? limit : kPolls; };
+    constexpr int SUMS = kSums<E, FMT>, PLACES = kPlaces<E, FMT>, COLUMNS = PLACES * SUMS * kMostTokens;  // of TMEM
     extern __shared__ uint8_t dyn[];
     __shared__ Shared S;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -82,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_barrier_init();
         tc::tma_prefetch(&tx);
     }
-    if (warp == 2) tc::tmem_alloc(&S.tmem, 256);
+    if (warp == 2) tc::tmem_alloc(&S.tmem, COLUMNS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -117,15 +125,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t id = tc::idesc(FMT16, 0, 0, kRows, q.nt);
         const uint64_t a0 = tc::operand_desc(tc::smem_u32(ring), false), b0 = tc::operand_desc(tc::smem_u32(ring) + 2 * kP, false);
         for (int p = 0; p < np; ++p) {
-            const int s = p % kStages;
-            if (!tc::mbar_spin(&S.acc_empty[s], (p / kStages & 1) ^ 1, err, polls(q.limit.mma))) break;
+            const int s = p % kStages, place = p % PLACES;
+            if (!tc::mbar_spin(&S.acc_empty[place], (p / PLACES & 1) ^ 1, err, polls(q.limit.mma))) break;
             if (!tc::mbar_spin(&S.full[s], p / kStages & 1, err, polls(q.limit.mma))) break;
             tc::fence_after_sync();
             if (lead) {
                 const uint64_t da = a0 + (uint32_t)(s * stage >> 4), db = b0 + (uint32_t)(s * stage >> 4);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    tc::mma<false, false>(tmem + s * kMostTokens, da + (k / 4 * kP >> 4) + k % 4 * 2, db + (k / 4 * q.q_bytes >> 4) + k % 4 * 2, id, k);
+                    tc::mma<false, false>(tmem + (place * SUMS + k * SUMS / 8) * kMostTokens, da + (k / 4 * kP >> 4) + k % 4 * 2,
+                                          db + (k / 4 * q.q_bytes >> 4) + k % 4 * 2, id, k % (8 / SUMS));
                 tc::mma_commit(&S.done[s]);
             }
             __syncwarp();
@@ -134,34 +143,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lead) tc::mma_commit(&S.drain);
         tc::mbar_wait(&S.drain, 0, err, PE_DEVERR_TIMEOUT, tc::kLeavePolls);
     } else if (warp >= 4 && warp < 12) {
-        // ---- sums: a lane has a weight row, a warp 32 tokens
-        const int quarter = warp & 3, c0 = (warp - 4) / 4 * 32, row = min(f0 + quarter * 32 + lane, a.N - 1);
+        // ---- sums: a lane has a weight row, a warp half of the tokens, 16 or 32
+        const int quarter = warp & 3, share = q.nt > 32 ? 32 : 16, c0 = (warp - 4) / 4 * share, row = min(f0 + quarter * 32 + lane, a.N - 1);
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-        const uint16_t* scales = static_cast<const uint16_t*>(a.scales) + (size_t)row * groups + p0;
         float acc[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[j] = 0.f;
-        uint16_t next = FMT == W4_INT4 && np > 0 ? scales[0] : 0;
+        // The raw scales of a pair's sums (past K, of nothing), two pairs ahead; what
+        // is loaded rests until its turn (fp16 with MXFP4, 32 x 4096 to 32000: 56 us;
+        // one pair ahead 77).
+        uint32_t raw[2][2] = {};
+        auto scales = [&](int p, uint32_t(&to)[2]) {
+            to[0] = to[1] = 0;
+            const int at = SUMS * (p0 + p);
+            if (p >= np) return;
+            if constexpr (FMT == W4_INT4) {
+                to[0] = static_cast<const uint16_t*>(a.scales)[(size_t)row * groups + at];
+            } else if constexpr (SUMS > 1) {
+                const uint8_t* from = static_cast<const uint8_t*>(a.scales) + (size_t)row * groups + at;
+                if (groups % 2 == 0) {
+                    to[0] = *reinterpret_cast<const uint16_t*>(from);
+                    if (at + 2 < groups) to[1] = *reinterpret_cast<const uint16_t*>(from + 2);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < SUMS; ++i)
+                        if (at + i < groups) to[i / 2] |= (uint32_t)from[i] << (8 * (i & 1));
+                }
+            }
+        };
+        scales(0, raw[0]);
+        scales(1, raw[1]);
         bool ok = true;
         for (int p = 0; p < np; ++p) {
-            const float s = FMT == W4_INT4 ? __half2float(__ushort_as_half(next)) : 1.f;
-            if (FMT == W4_INT4 && p + 1 < np) next = scales[p + 1];
-            const int buf = p % kStages;
-            if (!(ok = tc::mbar_spin(&S.done[buf], p / kStages & 1, err, polls(q.limit.sums)))) break;
+            const uint32_t bits = raw[0][0] | raw[0][1] << 16;
+            raw[0][0] = raw[1][0], raw[0][1] = raw[1][1];
+            scales(p + 2, raw[1]);
+            if (!(ok = tc::mbar_spin(&S.done[p % kStages], p / kStages & 1, err, polls(q.limit.sums)))) break;
             tc::fence_after_sync();
+            const int place = p % PLACES;
             if (c0 < q.nt) {
 #pragma unroll
-                for (int h = 0; h < 32; h += 16) {
-                    uint32_t r[16];
-                    tc::tmem_ld16(lanes + buf * kMostTokens + h, r);
-                    tc::tmem_ld_wait(r);
+                for (int i = 0; i < SUMS; ++i) {
+                    const float f = FMT == W4_INT4 ? __half2float(__ushort_as_half((unsigned short)bits))
+                                    : SUMS > 1   ? e8m0(bits >> (8 * i) & 255u)
+                                                 : 1.f;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[h + j] = fmaf(s, __uint_as_float(r[j]), acc[h + j]);
+                    for (int h = 0; h < 32; h += 16) {
+                        if (h >= share) continue;
+                        uint32_t r[16];
+                        tc::tmem_ld16(lanes + (place * SUMS + i) * kMostTokens + h, r);
+                        tc::tmem_ld_wait(r);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[h + j] = fmaf(f, __uint_as_float(r[j]), acc[h + j]);
+                    }
                 }
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&S.acc_empty[buf]);
+            if (lane == 0) tc::mbar_arrive(&S.acc_empty[place]);
         }
         const float ts = FMT == W4_NVFP4 ? a.tensor_scale[0] : 1.f;
         // every warp is past its last buffer, so every MMA is done with the ring
@@ -170,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (c0 + j < q.nt) part[j * kRows] = acc[j] * ts;
+                if (j < share && c0 + j < q.nt) part[j * kRows] = acc[j] * ts;
     } else if (warp >= 12) {
         // ---- decoding: lanes 2 i and 2 i + 1 have 64 inputs of a row, 16 rows a warp
         const int half = lane & 1, r0 = (warp - 12) % kDecoders * 16 + (lane >> 1), set = (warp - 12) / kDecoders;
@@ -185,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 to.s[b] = 0;
                 if (p < np && k < a.K) {  // K is a multiple of 32; the tokens' copy has zeros past it
                     to.w[b] = *reinterpret_cast<const int4*>(codes + (p0 + p) * 64 + 32 * b);
-                    if (FMT == W4_MXFP4) to.s[b] = scales[k / 32];
+                    if (FMT == W4_MXFP4 && SUMS == 1) to.s[b] = scales[k / 32];
                     if (FMT == W4_NVFP4) to.s[b] = *reinterpret_cast<const uint16_t*>(scales + k / 16);
                 }
             }
@@ -208,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float f[2];
-                    if (FMT == W4_MXFP4) {
-                        f[0] = f[1] = in_range<E>(e8m0(c[h].s[b]));
+                    if (FMT == W4_MXFP4 && SUMS == 1) {
+                        f[0] = f[1] = e8m0(c[h].s[b]);
                     } else if (FMT == W4_NVFP4) {
                         const float2 v = e4m3x2(c[h].s[b]);
                         f[0] = v.x, f[1] = v.y;
@@ -220,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t word = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
                         uint32_t v[4];
                         if (FMT == W4_INT4) int4x8<E>(word, v);
+                        else if (SUMS > 1) e2m1x8<E>(word, v);
                         else e2m1x8<E>(word, Pair<E>::both(f[j / 2]), v);
                         // (0, 4) (1, 5) (2, 6) (3, 7) to the inputs' order
                         uint4 o;
@@ -251,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::cluster_wait();
     }
     tc::fence_after_sync();
-    if (warp == 2) tc::tmem_dealloc(tmem, 256);
+    if (warp == 2) tc::tmem_dealloc(tmem, COLUMNS);
 }
 
 // CTAs along K: as many as fill the SMs in one wave, four at most (32 rows,

@@ -5,10 +5,50 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import dense_ref as R  # noqa: E402
 import experts_ref as X  # noqa: E402
-from test_gpu_experts import F32, HF, D, ints  # noqa: E402, F401
+from test_gpu_experts import F32, FMTS, HF, D, ints, rand, weights  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16, 17, 64, 96, 128])
+def test_every_mxfp4_scale_with_fp16(D, rows):  # noqa: F811
+    """Rows of the identity pick single weights out of groups whose scales lie
+    as far apart as E8M0 goes: each is what fp32 holds of it, and a scale beyond
+    fp16 meets inputs of zero without a word."""
+    k, n = 160, 41
+    codes, s = ints(0, 256, (n, k // 2)), ints(0, 255, (n, k // 32), seed=1)
+    s[:8] = torch.arange(136, 144, device="cuda")[:, None]  # about where fp16 ends
+    s[8:16] = torch.arange(100, 108, device="cuda")[:, None]  # and begins
+    want = X.values(codes, s, "mxfp4").t().float()  # the nearest, infinity past the largest
+    eye = torch.eye(k, device="cuda", dtype=HF)
+    for a in range(0, k, rows):
+        a = min(a, k - rows)
+        assert torch.equal(D.linear_w4(eye[a : a + rows], codes, s, "mxfp4", out_dtype=F32), want[a : a + rows])
+
+
+@pytest.mark.parametrize("rows,k,n", [(3, 224, 40), (16, 1056, 72), (40, 1056, 72), (128, 352, 200)])
+def test_large_and_small_mxfp4_scales_with_fp16(D, rows, k, n):  # noqa: F811
+    for lo, hi in ((141, 160), (80, 104)):
+        codes, s = ints(0, 256, (n, k // 2)), ints(lo, hi, (n, k // 32), seed=lo)
+        x = rand(rows, k, dt=HF)
+        y = D.linear_w4(x, codes, s, "mxfp4", out_dtype=F32)
+        R.check(y, X.linear_w4(x, X.values(codes, s, "mxfp4"), None, "none", None, HF, F32, False), "y")
+
+
+def test_nan_scales_with_fp16(D):  # noqa: F811
+    k, n = 160, 24
+    for fmt in FMTS:
+        c, s, ts = weights(fmt, n, k)
+        s = s.clone()
+        if fmt == "int4":
+            s[5, 1] = float("nan")
+        else:
+            s.view(torch.uint8)[5, 4] = 255 if fmt == "mxfp4" else 127
+        for rows in (3, 16, 40, 150):
+            y = D.linear_w4(rand(rows, k, dt=HF), c, s, fmt, tensor_scale=ts)
+            assert y[:, 5].isnan().all() and torch.isfinite(y[:, :5]).all() and torch.isfinite(y[:, 6:]).all()
 
 
 def test_mxfp4_weights_unpacked_to_fp16(D):  # noqa: F811
