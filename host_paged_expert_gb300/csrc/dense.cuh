@@ -33,7 +33,10 @@ enum EpiKind {
     EPI_LINEAR = 0,     // act(v + bias) + residual; optionally v + bias is kept
     EPI_GATED = 1,      // act(gate) * up of two accumulators; optionally both are kept
     EPI_GATED_BWD = 2,  // from dh and the kept gate and up: their gradients and h
+    EPI_SCALED = 3,     // EPI_LINEAR of v times a factor
 };
+// What an epilogue does once v is there.
+constexpr int after_factor(int kind) { return kind == EPI_SCALED ? (int)EPI_LINEAR : kind; }
 
 struct Epi {
     int act;             // pe_act
@@ -49,6 +52,7 @@ struct Epi {
     int64_t ld_keep;
     const void* gu;      // EPI_GATED_BWD: [rows, 2 cols] kept gate and up
     void* h;             // EPI_GATED_BWD: [rows, cols], or NULL
+    const float* factor; // EPI_SCALED: one number
 };
 
 // One matrix product C[m, n] = sum_k A(m, k) B(n, k) with an epilogue.  A

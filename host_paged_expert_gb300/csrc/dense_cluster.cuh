@@ -28,7 +28,8 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
     // the stride between a thread's units is a multiple of U: its columns stay the same
     const int u0 = (int)threadIdx.x, col = f0 + (u0 % U) * 8;
     float bias[8];
-    epi_cols<E, KIND>(e, col, bias);
+    epi_cols<E, after_factor(KIND)>(e, col, bias);
+    const float factor = KIND == EPI_SCALED ? e.factor[0] : 1.f;
     for (int ub = u0; ub < total; ub += THREADS * BATCH) {
         float v[BATCH][G][8];
         EpiIn in[BATCH];
@@ -36,7 +37,7 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
         for (int i = 0; i < BATCH; ++i) {
             const int u = ub + i * THREADS, t = r0 + u / U;
             const uint32_t at = (uint32_t)(t * kRows + (u0 % U) * 8) * 4;
-            in[i] = epi_load<E, KIND>(e, u < total ? t0 + t : e.rows, col);
+            in[i] = epi_load<E, after_factor(KIND)>(e, u < total ? t0 + t : e.rows, col);
             if (u >= total) continue;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -56,6 +57,9 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
                         float* d = v[i][g] + 4 * h;
                         d[0] += a[r][h].x, d[1] += a[r][h].y, d[2] += a[r][h].z, d[3] += a[r][h].w;
                     }
+                if (KIND == EPI_SCALED)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][g][j] *= factor;
             }
         }
         with_act(e.act, [&](auto act) {
@@ -63,10 +67,10 @@ __device__ __forceinline__ void reduce(const Epi& e, const uint8_t* ring, int nt
             for (int i = 0; i < BATCH; ++i) {
                 const int u = ub + i * THREADS;
                 if (u < total) {
-                    if (epi_light<KIND>(e))
+                    if (epi_light<after_factor(KIND)>(e))
                         epi_store_light<E, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0]);
                     else
-                        epi_store<E, KIND, decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0], v[i][G - 1]);
+                        epi_store<E, after_factor(KIND), decltype(act)::value>(e, t0 + r0 + u / U, col, bias, in[i], v[i][0], v[i][G - 1]);
                 }
             }
         });

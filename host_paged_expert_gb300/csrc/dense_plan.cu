@@ -56,7 +56,7 @@ constexpr PairCost kWide = {5.2, 0.1, 0.265, 0.5, 2.65, 0.11, 2.7}, kNarrow = {3
 // as a plain one.
 double epi_extra(const Product& p, EpiKind kind, int tn) {
     if (kind == EPI_GATED) return tn == 128 ? 0.7 : 0.0;
-    if (kind != EPI_LINEAR) return 0;
+    if (after_factor(kind) != EPI_LINEAR) return 0;
     return (p.e.act != PE_ACT_NONE ? 0.8 : 0.0) + (p.e.bias ? 0.2 : 0.0) + (p.e.res ? 0.9 : 0.0) + (p.e.keep ? 0.5 : 0.0) +
            (p.e.out_f32 ? 0.9 : 0.0);
 }
@@ -136,7 +136,7 @@ Choice choose(const Product& p, EpiKind kind) {
             if (fits > bounded || (fits == bounded && us < c.us)) c.us = us, c.tn = 0, c.shape = s, bounded = fits;
         }
     }
-    if (p.M <= kGemvRows && !p.a_mn && !p.b_mn && kind != EPI_GATED_BWD) {
+    if (p.M <= kGemvRows && !p.a_mn && !p.b_mn && kind <= EPI_GATED) {
         const double us = gemv_time(p);
         if (us < c.us) c.us = us, c.gemv = true;
     }

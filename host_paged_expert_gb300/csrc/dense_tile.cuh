@@ -23,13 +23,21 @@ __device__ __forceinline__ void patch_get(const uint8_t* patch, int r, int c8, f
 // block's accumulators are there.
 template <typename E, int KIND>
 struct Ahead {
-    float bias[8];
+    float factor, bias[8];
     EpiIn in[4];
     __device__ __forceinline__ void load(const Epi& e, int lane, int row0, int col0) {
         const int col = col0 + 8 * (lane & 3);
-        epi_cols<E, KIND>(e, col, bias);
+        factor = KIND == EPI_SCALED ? e.factor[0] : 1.f;
+        epi_cols<E, after_factor(KIND)>(e, col, bias);
 #pragma unroll
-        for (int it = 0; it < 4; ++it) in[it] = epi_load<E, KIND>(e, row0 + it * 8 + (lane >> 2), col);
+        for (int it = 0; it < 4; ++it) in[it] = epi_load<E, after_factor(KIND)>(e, row0 + it * 8 + (lane >> 2), col);
+    }
+    // eight columns of a row of the patch
+    __device__ __forceinline__ void get(const uint8_t* patch, int r, int c8, float (&v)[8]) const {
+        patch_get(patch, r, c8, v);
+        if (KIND == EPI_SCALED)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= factor;
     }
 };
 
@@ -39,20 +47,20 @@ __device__ __forceinline__ void patch_out(const Epi& e, const uint8_t* patch, in
     const int c8 = lane & 3, row = row0 + (lane >> 2), col = col0 + 8 * c8;
     with_act(e.act, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        if (epi_light<KIND>(e)) {
+        if (epi_light<after_factor(KIND)>(e)) {
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 float v[8];
-                patch_get(patch, it * 8 + (lane >> 2), c8, v);
+                x.get(patch, it * 8 + (lane >> 2), c8, v);
                 epi_store_light<E, ACT>(e, row + it * 8, col, x.bias, x.in[it], v);
             }
         } else {
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 float v[8], u[8];
-                patch_get(patch, it * 8 + (lane >> 2), c8, v);
+                x.get(patch, it * 8 + (lane >> 2), c8, v);
                 if (KIND == EPI_GATED) patch_get(patch + 4096, it * 8 + (lane >> 2), c8, u);
-                epi_store<E, KIND, ACT>(e, row + it * 8, col, x.bias, x.in[it], v, u);
+                epi_store<E, after_factor(KIND), ACT>(e, row + it * 8, col, x.bias, x.in[it], v, u);
             }
         }
     });

@@ -94,7 +94,7 @@ struct W4Args {
 constexpr int kW4Stream = 16, kW4Rows = 128;
 cudaError_t launch_w4(const W4Args& a, int elem, cudaStream_t st);
 cudaError_t launch_w4_tc(const W4Args& a, int elem, uint32_t* err, cudaStream_t st, const WaitLimits* limits = nullptr);
-// w [N, K] of the element type = codes times scales
+// w [N, K] of the element type = codes times scales, without the tensor's
 cudaError_t launch_w4_unpack(const W4Args& a, void* w, int elem, cudaStream_t st);
 
 }  // namespace dense

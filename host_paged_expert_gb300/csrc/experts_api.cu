@@ -400,7 +400,8 @@ extern "C" pe_status pe_linear_four_bit(const void* x, int64_t x_stride, const v
         p.N = out_features;
         p.K = in_features;
         p.e = a.e;
-        e = launch_product(p, EPI_LINEAR, elem, CHAIN_NONE, err, st);
+        p.e.factor = tensor_scale;
+        e = launch_product(p, fmt == W4_NVFP4 ? EPI_SCALED : EPI_LINEAR, elem, CHAIN_NONE, err, st);
     }
     return done(e);
 }

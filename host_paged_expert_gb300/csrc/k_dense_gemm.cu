@@ -433,6 +433,9 @@ cudaError_t launch_kind(const Product* p, int count, EpiKind kind, int tn, uint3
     if (kind == EPI_LINEAR)
         return tn == 256 ? launch<E, EPI_LINEAR, false, 256>(p, count, err, st)
                          : launch<E, EPI_LINEAR, false, 128>(p, count, err, st);
+    if (kind == EPI_SCALED)
+        return tn == 256 ? launch<E, EPI_SCALED, false, 256>(p, count, err, st)
+                         : launch<E, EPI_SCALED, false, 128>(p, count, err, st);
     if (kind == EPI_GATED)
         return tn == 256 ? launch<E, EPI_GATED, false, 256>(p, count, err, st)
                          : launch<E, EPI_GATED, false, 128>(p, count, err, st);

@@ -183,7 +183,7 @@ cudaError_t launch_kind(const Product& p, EpiKind kind, int chain, cudaStream_t 
 }  // namespace
 
 cudaError_t launch_gemv(const Product& p, EpiKind kind, int elem, int chain, cudaStream_t st) {
-    if (p.M > kGemvRows || p.a_mn || p.b_mn || kind == EPI_GATED_BWD) return cudaErrorInvalidValue;
+    if (p.M > kGemvRows || p.a_mn || p.b_mn || kind > EPI_GATED) return cudaErrorInvalidValue;
     return elem == PE_ELEM_BF16 ? launch_kind<__nv_bfloat16>(p, kind, chain, st) : launch_kind<__half>(p, kind, chain, st);
 }
 

@@ -371,6 +371,7 @@ template <typename E>
 cudaError_t launch_kind(const Product& p, EpiKind kind, const SplitShape& s, int chain, uint32_t* err, cudaStream_t st) {
     if (p.a_scale) return launch<E, EPI_LINEAR, true>(p, s, chain, err, st);
     if (kind == EPI_LINEAR) return launch<E, EPI_LINEAR, false>(p, s, chain, err, st);
+    if (kind == EPI_SCALED) return launch<E, EPI_SCALED, false>(p, s, chain, err, st);
     if (kind == EPI_GATED) return launch<E, EPI_GATED, false>(p, s, chain, err, st);
     return launch<E, EPI_GATED_BWD, false>(p, s, chain, err, st);
 }

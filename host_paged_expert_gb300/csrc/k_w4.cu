@@ -26,7 +26,8 @@
 // end.  MXFP4's scales reach past fp16 at both ends: with it they multiply sums
 // of their 32 inputs, and a lane takes eight codes of each group instead of a
 // group's 32.  So weights are not rounded at all.  Above kW4Rows they are unpacked
-// to 16 bits for the dense products' kernels, which rounds int4's and NVFP4's once.
+// to 16 bits for the dense products' kernels, which rounds int4's once, and
+// MXFP4's where fp16 ends.
 #include "experts.cuh"
 #include "fp8_device.cuh"
 #include "pe_device.cuh"
@@ -248,14 +249,14 @@ __global__ void __launch_bounds__(W * 32) w4_kernel(const __grid_constant__ W4Ar
     });
 }
 
-// Eight codes a thread: 4096 x 4096 in 7 us, the rate of HBM though L2 holds it.
+// NVFP4 without the tensor's scale, which multiplies the product's sums.  Eight
+// codes a thread: 4096 x 4096 in 7 us, the rate of HBM though L2 holds it.
 template <typename E, int FMT>
 __global__ void __launch_bounds__(256) w4_unpack_kernel(const __grid_constant__ W4Args a, E* out) {
     pdl_wait();
     pdl_trigger();
     const int groups = (a.K + w4_group(FMT) - 1) / w4_group(FMT), words = a.K / 8;
     const int64_t total = (int64_t)a.N * words;
-    const float ts = FMT == W4_NVFP4 ? a.tensor_scale[0] : 1.f;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t n = i / words;
         const int k = (int)(i - n * words) * 8;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const __grid_constant__ 
         float s;
         if (FMT == W4_INT4) s = __half2float(static_cast<const __half*>(a.scales)[at]);
         else if (FMT == W4_MXFP4) s = 0.5f * e8m0(static_cast<const uint8_t*>(a.scales)[at]);
-        else s = 0.5f * ts * e4m3x2(static_cast<const uint8_t*>(a.scales)[at]).x;
+        else s = 0.5f * e4m3x2(static_cast<const uint8_t*>(a.scales)[at]).x;
         float v[8];
         if (FMT == W4_INT4) {
 #pragma unroll

@@ -565,10 +565,10 @@ pe_status pe_grouped_ffn_backward(const void* dy, int64_t dy_stride, const void*
  *     [out, in/32]; NVFP4: E4M3 [out, in/16], times tensor_scale[0] (device; NULL
  *     for the other formats).
  * Up to 128 rows the weights are used unrounded, whatever their scales; above,
- * they are unpacked to elem in the workspace first: int4's and NVFP4's products
- * with their scales are rounded there.  With fp16 a weight is then what fp16
- * holds of it: infinite from 65520 on, without its last bits below 2^-14, zero up
- * to 2^-25.
+ * they are unpacked to elem in the workspace first: int4's products with their
+ * scales are rounded there (NVFP4's tensor scale multiplies fp32 sums at any
+ * number of rows).  With fp16 an int4 or MXFP4 weight is then what fp16 holds of
+ * it: infinite from 65520 on, without its last bits below 2^-14, zero up to 2^-25.
  * in: a multiple of 32.
  * workspace: pe_linear_four_bit_workspace(rows, in, out) bytes. */
 size_t pe_linear_four_bit_workspace(int32_t rows, int32_t in_features, int32_t out_features);

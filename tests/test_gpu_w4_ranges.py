@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 
 import dense_ref as R  # noqa: E402
 import experts_ref as X  # noqa: E402
-from test_gpu_experts import F32, FMTS, HF, D, ints, rand, weights  # noqa: E402, F401
+from test_gpu_experts import BF, F32, FMTS, HF, D, ints, rand, weights  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,22 @@ def test_mxfp4_weights_unpacked_to_fp16(D):  # noqa: F811
     want = X.values(codes, e, "mxfp4").half().t().float()
     assert torch.isfinite(want).all()
     assert torch.equal(D.linear_w4(torch.eye(k, device="cuda", dtype=HF), codes, e, "mxfp4", out_dtype=F32), want)
+
+
+@pytest.mark.parametrize("rows", [128, 129, 300, 1024])
+@pytest.mark.parametrize("k,n", [(1056, 200), (96, 77), (512, 2048)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_tensor_scales_of_any_size(D, rows, k, n, dt):  # noqa: F811
+    """They multiply sums: no weight is rounded, at any number of rows."""
+    codes, s, _ = weights("nvfp4", n, k)
+    x, b, res = rand(rows, k, dt=dt), rand(n, seed=2, dt=dt), rand(rows, n, seed=3, dt=dt)
+    for scale in (2.0**-20, 0.0123, 2.0**18):
+        ts = torch.full((1,), scale, device="cuda")
+        w = X.values(codes, s, "nvfp4", ts)
+        y = D.linear_w4(x, codes, s, "nvfp4", tensor_scale=ts, out_dtype=F32)
+        R.check(y, X.linear_w4(x, w, None, "none", None, dt, F32, False), f"y at {scale}")
+    ts = torch.full((1,), 0.0123, device="cuda")
+    w = X.values(codes, s, "nvfp4", ts)
+    for act in ("none", "silu"):
+        y = D.linear_w4(x, codes, s, "nvfp4", b, act, res, tensor_scale=ts)
+        R.check(y, X.linear_w4(x, w, b, act, res, dt, dt, False), act)
