@@ -17,8 +17,9 @@
 //
 // Bound by a block's latency (a launch, its first loads, three or four chunks, the
 // sum over warps), and where weights are many by the rate of integer and logic
-// instructions, which decoding is made of: 1 x 2048 to 2048 int4 2.6 us, 1 x 4096
-// to 4096 5.0, 8 x 4096 to 4096 nvfp4 6.0, 1 x 8192 to 8192 int4 12.6 (floor 5).
+// instructions, which decoding is made of.  Weights in L2: 1 x 2048 to 2048 int4 2.6
+// us, 1 x 4096 to 4096 5.0, 8 x 4096 to 4096 nvfp4 6.0, 1 x 8192 to 8192 int4 12.6
+// (floor 5); from HBM the last three 5.7, 6.6 and 14.1.
 //
 // Rounding: int4's q - 8 and E2M1 times its block scale are exact in 16 bits
 // (a 2-bit times a 4-bit significand, or a power of two), int4's scales

@@ -15,10 +15,14 @@
 // exact in 16 bits.  But MXFP4's scales reach past fp16: with it a pair has four
 // buffers, one for each 32 inputs, and their scales multiply them too.
 //
-// Bound by the MMAs, which take about 110 cycles for 128 rows and 16 inputs
-// whatever the tokens, 0.48 of a pair's 0.53 us (without decoding anything it
-// took as long; with a barrier each for weights and tokens, and for every block,
-// 0.65): 32 x 4096 to 4096 10.1 us, 32 x 4096 to 32000 39 to 44.
+// Bound by the decoding warps, their instructions and the latency of their
+// loads.  NVFP4, 32 x 8192 to 19456 (152 tiles, one a CTA; 64 pairs of blocks):
+// 44.5 us.  With two of a pair's eight MMAs 43.2, without the sums 43.8, without
+// writing what is decoded 45.8; without the arithmetic of decoding 34.1, with the
+// first codes loaded only 35.7.  (A chain of MMAs alone takes 72 cycles for 128
+// rows, 16 inputs and up to 32 tokens, 77 for 64, 85 for 128 and 129 for 256: 0.28
+// us of a pair's 0.69.)  Weights in L2, 32 x 4096 to 4096 10 to 11 us, to 32000 40
+// to 48; from HBM 10.4 (int4) and 46 to 49.
 #include "experts.cuh"
 #include "dense_cluster.cuh"
 #include "dense_tc.cuh"
