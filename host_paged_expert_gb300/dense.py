@@ -178,7 +178,7 @@ def linear_w4(x, codes, scales, fmt: str, bias=None, act: str = "none", residual
     E4M3 [out, in / 16] (uint8 or float8_e4m3fn) times ``tensor_scale`` fp32 [1].
     ``out_dtype=torch.float32`` leaves the result unrounded.  Up to 128 rows no
     weight is rounded; above, int4's are rounded to x's type, and with fp16 MXFP4's
-    and int4's have to lie in its range.  All but tensor_scale start at 16-byte
+    and int4's have to lie in its range.  All but ``tensor_scale`` start at 16-byte
     boundaries."""
     return (_native or _c()).linear_w4(x, codes, scales, fmt, bias, act, residual, tensor_scale, out_dtype, stream)
 
